@@ -268,31 +268,30 @@ PLAIN = {"scan_step": _scan_step, "scan_prompts": _scan_prompts, "scan_train": _
 # -- the framework's calls -----------------------------------------------------------------------------------------
 
 def _calls(s):
-    from recurrent_state_update_deltalog_b200 import (block_norm, gated_scan, gated_scan_prefill, gated_scan_step,
-                                                      paged_attention)
+    import recurrent_state_update_deltalog_b200 as dl
     op = s["case"]["op"]
     if op == "scan_step":
-        h = gated_scan_step(s["x"], s["log_decay"], s["state"], slot_idx=s["slot_idx"], new_state=s["new_state"])
+        h = dl.gated_scan_step(s["x"], s["log_decay"], s["state"], slot_idx=s["slot_idx"], new_state=s["new_state"])
         return [h, s["new_state"]]
     if op == "scan_prompts":
-        h = gated_scan_prefill(s["x"], s["log_decay"], s["state"], s["cu"], slot_idx=s["slot_idx"], zero_state=True)
+        h = dl.gated_scan_prefill(s["x"], s["log_decay"], s["state"], s["cu"], slot_idx=s["slot_idx"], zero_state=True)
         return [h, s["state"]]
     if op == "scan_train":
         ins = (s["x"], s["log_decay"], s["h0"])
-        h, last = gated_scan(*ins)
+        h, last = dl.gated_scan(*ins)
         return [h.detach(), last.detach(), *torch.autograd.grad((h, last), ins, (s["dh"], s["dlast"]))]
     if op == "norm_join":
-        return list(block_norm(s["y"], s["post"], gate=s["gate"], scale=s["scale"], residual=s["residual"],
+        return list(dl.block_norm(s["y"], s["post"], gate=s["gate"], scale=s["scale"], residual=s["residual"],
                                pre_weight=s["pre"], eps=EPS))
     if op == "norm_train":
-        out, normed = block_norm(s["y"], s["post"], gate=s["gate"], scale=s["scale"], residual=s["residual"],
+        out, normed = dl.block_norm(s["y"], s["post"], gate=s["gate"], scale=s["scale"], residual=s["residual"],
                                  pre_weight=s["pre"], eps=EPS)
         ins = tuple(s[k] for k in ("y", "gate", "residual", "post", "scale", "pre"))
         return [out.detach(), normed.detach(), *torch.autograd.grad((out, normed), ins, (s["dout"], s["dnormed"]))]
     if op == "norm_heads":
-        out = block_norm(s["y"], s["post"], gate=s["gate"], groups=s["case"]["H"], eps=EPS)
+        out = dl.block_norm(s["y"], s["post"], gate=s["gate"], groups=s["case"]["H"], eps=EPS)
         return [out.detach(), *torch.autograd.grad(out, (s["y"], s["gate"], s["post"]), s["dout"])]
-    o = paged_attention(s["q"], s["k_pages"], s["v_pages"], s["table"], s["lens"], k=s["k"], v=s["v"],
+    o = dl.paged_attention(s["q"], s["k_pages"], s["v_pages"], s["table"], s["lens"], k=s["k"], v=s["v"],
                         window=s["case"]["window"])
     return [o, s["k_pages"], s["v_pages"]]
 
