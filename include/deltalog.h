@@ -390,6 +390,62 @@ int dl_decode_static(int op, int B, int H, int d_k, int d_v, int M, int in_dtype
                      const float* log_decay, const float* beta, void* o, int* dev_err,
                      void* stream);
 
+/* ---- Operators beside the recurrent layers --------------------------------
+ * Stateless calls: no handle, every buffer is the caller's, nothing is
+ * allocated, each call is asynchronous on `stream` and runs on the current
+ * device.  They share these conventions.  in_dtype (DL_F32 or DL_BF16) is the
+ * type of the tensors called "typed"; float tensors are fp32.  All tensors
+ * are C-contiguous and aligned to their element size; 16-byte aligned ones
+ * with even sizes move fastest.  A slot map (slot_idx, device int32 [rows], or
+ * NULL: row r is slot r) follows dl_step_indexed: a negative entry, and one
+ * with DL_SLOT_HOLD set, is skipped (nothing read, nothing written); an
+ * entry >= slots is skipped and raises DL_DEVERR_SLOT_INDEX.  dev_err is NULL
+ * or a device int, cleared by the caller, that kernels OR their DL_DEVERR_*
+ * bits into; with NULL the rows concerned are skipped all the same.  rows is
+ * at most 65535.  Results are deterministic: no sum depends on the order in
+ * which blocks run. */
+
+/* Gated linear recurrence: the elementwise member of the family above, per
+ * channel
+ *     h_t = a_t h_{t-1} + x_t,   a_t = exp(log_decay_t),
+ * over packed sequences; log_decay <= 0 (-inf forgets the state).
+ *   cu_seqlens  device int32 [rows + 1] as in dl_prefill (an invalid range
+ *               skips the row and raises DL_DEVERR_SEQLEN), or NULL: every row
+ *               has total / rows tokens (total a multiple of rows);
+ *   x, h        typed [total][C] (h may be x);  log_decay float [total][C];
+ *   h0          float [slots][C], the states before the first tokens, or NULL
+ *               (zeros);  h_last: float [slots][C], receives the states after
+ *               the last tokens, or NULL; h_last may be h0.  A row without
+ *               tokens hands its state on.  Rows must name distinct slots;
+ *   ckpt        NULL, or float [total / DL_SCAN_CHUNK + rows][C] that keeps
+ *               the state before every DL_SCAN_CHUNK tokens of each row (row r
+ *               from entry cu_seqlens[r] / DL_SCAN_CHUNK + r on) for
+ *               dl_scan_backward.
+ * States, products of decays and sums are fp32; h is rounded once. */
+#define DL_SCAN_CHUNK 64
+int dl_scan(const int* slot_idx, int slots, int rows, const int* cu_seqlens, long long total, int C,
+            int in_dtype, const void* x, const float* log_decay, const float* h0, float* h_last,
+            void* h, float* ckpt, int* dev_err, void* stream);
+
+/* Backward pass of dl_scan without a slot map: from dh (typed [total][C]) and
+ * dh_last (float [rows][C] or NULL: zeros),
+ *     G_t = dh_t + a_{t+1} G_{t+1}  (the last token's: dh_t + dh_last),
+ *     dx_t = G_t,  dlog_decay_t = a_t h_{t-1} G_t,  dh0 = a_0 G_0.
+ * dx is typed, dlog_decay float [total][C], dh0 float [rows][C] or NULL.
+ * ckpt is what dl_scan left for the same x, log_decay, h0 and rows; h itself
+ * is not needed. */
+int dl_scan_backward(int rows, const int* cu_seqlens, long long total, int C, int in_dtype,
+                     const void* x, const float* log_decay, const float* ckpt, const void* dh,
+                     const float* dh_last, void* dx, float* dlog_decay, float* dh0, int* dev_err,
+                     void* stream);
+
+/* One token of dl_scan for every row: x, h typed [rows][C], log_decay float
+ * [rows][C], state and new_state float [slots][C] (new_state may be state;
+ * slots that no row names are not written). */
+int dl_scan_step(const int* slot_idx, int slots, int rows, int C, int in_dtype, const void* x,
+                 const float* log_decay, const float* state, float* new_state, void* h,
+                 int* dev_err, void* stream);
+
 /* Bits of the device error word. */
 enum dl_device_error {
   DL_DEVERR_WAIT_TIMEOUT = 1,  /* a bounded wait gave up (a log copy in a step: that unit wrote
@@ -398,7 +454,7 @@ enum dl_device_error {
                                   when the hardware did not finish work it was given within a
                                   second; treat the CUDA context as suspect afterwards */
   DL_DEVERR_SLOT_INDEX = 2,    /* a slot index >= B (indexed steps, dl_prefill) */
-  DL_DEVERR_SEQLEN = 4         /* dl_prefill: a row's cu_seqlens range is invalid */
+  DL_DEVERR_SEQLEN = 4         /* a row's cu_seqlens range is invalid (dl_prefill, dl_scan) */
 };
 
 /* Read and clear the handle's device error word in one atomic step on

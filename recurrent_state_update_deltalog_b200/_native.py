@@ -19,6 +19,8 @@ DL_M_AUTO = 0
 DL_PREFILL_ZERO_STATE = 1
 DL_STATIC_SCRATCH_BYTES = 16 << 20
 DL_SLOT_HOLD = 0x40000000
+DL_SCAN_CHUNK = 64
+DL_DEVERR_SLOT_INDEX, DL_DEVERR_SEQLEN = 2, 4
 DL_OPT_STEP_KERNEL = 0
 DL_OPT_HOST_PREFETCH = 1
 DL_OPT_PDL = 2
@@ -59,6 +61,9 @@ SIGNATURES = {
     "dl_slot_read": (_I, [_P, _I, _P, _P]),
     "dl_check_device": (_I, [_P, _P]),
     "dl_decode_static": (_I, [_I, _I, _I, _I, _I, _I, _I, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "dl_scan": (_I, [_P, _I, _I, _P, ctypes.c_longlong, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "dl_scan_backward": (_I, [_I, _P, ctypes.c_longlong, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "dl_scan_step": (_I, [_P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P]),
     "dl_strerror": (ctypes.c_char_p, [_I]),
     "dl_last_error": (ctypes.c_char_p, []),
 }

@@ -1,0 +1,174 @@
+// Entry points of the gated linear recurrence (kernels in scan.cuh).
+#include "scan.cuh"
+
+#include <limits.h>
+
+#include <initializer_list>
+
+namespace {
+
+using dl::ScanArgs;
+
+int bad(const char* msg) { return dl::record_error(DL_ERR_ARG, msg); }
+
+// Channels of one lane: two neighbours when every row of every tensor starts
+// on that many elements' alignment, else one.
+int vec_of(int C, int dtype, std::initializer_list<const void*> typed, std::initializer_list<const void*> f32) {
+  if (C % 2) return 1;
+  for (const void* p : typed)
+    if (p && !dl::is_aligned(p, dtype == DL_BF16 ? 4 : 8)) return 1;
+  for (const void* p : f32)
+    if (p && !dl::is_aligned(p, 8)) return 1;
+  return 2;
+}
+
+// CTAs along time: enough that the launch has about four CTAs an SM, no more
+// than the sequences have chunks of 64 tokens on average.
+int cluster_of(long long tiles, int rows, long long total) {
+  const long long chunks = (total / rows + dl::kScanChunk - 1) / dl::kScanChunk;
+  int n = 1;
+  while (n < 8 && 2 * n <= chunks && tiles * rows * n < 4 * 148) n *= 2;
+  return n;
+}
+
+int check_common(int rows, long long total, int C, int dtype, const int* cu, const int* slot_idx) {
+  if (dtype != DL_F32 && dtype != DL_BF16) return bad("unknown dtype");
+  if (C < 1 || C > (1 << 24)) return bad("C outside [1, 2^24]");
+  if (rows < 0 || total < 0) return bad("negative rows or total");
+  if (rows > 65535) return dl::record_error(DL_ERR_UNSUPPORTED, "at most 65535 rows (grid y)");
+  if (rows == 0 && total > 0) return bad("tokens without rows");
+  if (cu && total > INT_MAX) return dl::record_error(DL_ERR_UNSUPPORTED, "cu_seqlens reach 2^31 - 1 tokens");
+  if (!cu && rows > 0 && total % rows) return bad("without cu_seqlens, total must be a multiple of rows");
+  if ((cu && !dl::is_aligned(cu, 4)) || (slot_idx && !dl::is_aligned(slot_idx, 4)))
+    return bad("index pointer not 4-byte aligned");
+  return DL_OK;
+}
+
+bool typed_ok(const void* p, int dtype) { return dl::is_aligned(p, dtype == DL_BF16 ? 2 : 4); }
+
+template <bool BACK, typename TX, int V>
+cudaError_t launch(const ScanArgs& a, int rows, cudaStream_t st) {
+  const long long tiles = (a.C + 32 * V - 1) / (32 * V);
+  const int n = cluster_of(tiles, rows, a.total);
+  const dim3 grid(static_cast<unsigned>(tiles * n), rows);
+  const int block = dl::kScanWarps * 32;
+  if constexpr (BACK) {
+    return n > 1 ? dl::launch_cluster(dl::scan_backward_kernel<TX, V, true>, grid, block, 0, st, n, a, n)
+                 : dl::launch_cluster(dl::scan_backward_kernel<TX, V, false>, grid, block, 0, st, 1, a, 1);
+  } else {
+    return n > 1 ? dl::launch_cluster(dl::scan_kernel<TX, V, true>, grid, block, 0, st, n, a, n)
+                 : dl::launch_cluster(dl::scan_kernel<TX, V, false>, grid, block, 0, st, 1, a, 1);
+  }
+}
+
+template <bool BACK>
+cudaError_t launch(const ScanArgs& a, int rows, int dtype, int vec, cudaStream_t st) {
+  if (dtype == DL_BF16)
+    return vec == 2 ? launch<BACK, __nv_bfloat16, 2>(a, rows, st) : launch<BACK, __nv_bfloat16, 1>(a, rows, st);
+  return vec == 2 ? launch<BACK, float, 2>(a, rows, st) : launch<BACK, float, 1>(a, rows, st);
+}
+
+template <typename TX, int V>
+cudaError_t launch_step(const ScanArgs& a, int rows, cudaStream_t st) {
+  const dim3 grid((a.C + 128 * V - 1) / (128 * V), rows);
+  dl::scan_step_kernel<TX, V><<<grid, 128, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+extern "C" {
+
+int dl_scan(const int* slot_idx, int slots, int rows, const int* cu_seqlens, long long total, int C, int in_dtype,
+            const void* x, const float* log_decay, const float* h0, float* h_last, void* h, float* ckpt, int* dev_err,
+            void* stream) {
+  const int rc = check_common(rows, total, C, in_dtype, cu_seqlens, slot_idx);
+  if (rc != DL_OK) return rc;
+  if (slot_idx ? slots < 1 : slots < rows) return bad("fewer slots than rows");
+  if (rows == 0) return DL_OK;
+  if (total > 0 && (!x || !log_decay || !h)) return bad("null input/output pointer");
+  if (!typed_ok(x, in_dtype) || !typed_ok(h, in_dtype)) return bad("input/output pointer not aligned to its element size");
+  if (!dl::is_aligned(log_decay, 4) || !dl::is_aligned(h0, 4) || !dl::is_aligned(h_last, 4) || !dl::is_aligned(ckpt, 4) ||
+      !dl::is_aligned(dev_err, 4))
+    return bad("fp32 pointer not 4-byte aligned");
+  ScanArgs a{};
+  a.x = x;
+  a.log_decay = log_decay;
+  a.h0 = h0;
+  a.h_last = h_last;
+  a.h = h;
+  a.ckpt = ckpt;
+  a.slot_idx = slot_idx;
+  a.cu = cu_seqlens;
+  a.err = dev_err;
+  a.total = total;
+  a.len = total / rows;
+  a.slots = slots;
+  a.C = C;
+  const cudaError_t e = launch<false>(a, rows, in_dtype, vec_of(C, in_dtype, {x, h}, {log_decay}),
+                                      static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? DL_OK : dl::launch_failed(e, "scan launch");
+}
+
+int dl_scan_backward(int rows, const int* cu_seqlens, long long total, int C, int in_dtype, const void* x,
+                     const float* log_decay, const float* ckpt, const void* dh, const float* dh_last, void* dx,
+                     float* dlog_decay, float* dh0, int* dev_err, void* stream) {
+  const int rc = check_common(rows, total, C, in_dtype, cu_seqlens, nullptr);
+  if (rc != DL_OK) return rc;
+  if (rows == 0) return DL_OK;
+  if (total > 0 && (!x || !log_decay || !ckpt || !dh || !dx || !dlog_decay)) return bad("null input/output pointer");
+  if (!typed_ok(x, in_dtype) || !typed_ok(dh, in_dtype) || !typed_ok(dx, in_dtype))
+    return bad("input/output pointer not aligned to its element size");
+  if (!dl::is_aligned(log_decay, 4) || !dl::is_aligned(ckpt, 4) || !dl::is_aligned(dh_last, 4) ||
+      !dl::is_aligned(dlog_decay, 4) || !dl::is_aligned(dh0, 4) || !dl::is_aligned(dev_err, 4))
+    return bad("fp32 pointer not 4-byte aligned");
+  ScanArgs a{};
+  a.x = x;
+  a.log_decay = log_decay;
+  a.ckpt = const_cast<float*>(ckpt);
+  a.cu = cu_seqlens;
+  a.dh = dh;
+  a.dh_last = dh_last;
+  a.dx = dx;
+  a.dlog_decay = dlog_decay;
+  a.dh0 = dh0;
+  a.err = dev_err;
+  a.total = total;
+  a.len = total / rows;
+  a.slots = rows;
+  a.C = C;
+  const cudaError_t e = launch<true>(a, rows, in_dtype, vec_of(C, in_dtype, {x, dh, dx}, {log_decay, dlog_decay}),
+                                     static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? DL_OK : dl::launch_failed(e, "scan backward launch");
+}
+
+int dl_scan_step(const int* slot_idx, int slots, int rows, int C, int in_dtype, const void* x, const float* log_decay,
+                 const float* state, float* new_state, void* h, int* dev_err, void* stream) {
+  const int rc = check_common(rows, rows, C, in_dtype, nullptr, slot_idx);
+  if (rc != DL_OK) return rc;
+  if (slot_idx ? slots < 1 : slots < rows) return bad("fewer slots than rows");
+  if (rows == 0) return DL_OK;
+  if (!x || !log_decay || !state || !new_state || !h) return bad("null input/output pointer");
+  if (!typed_ok(x, in_dtype) || !typed_ok(h, in_dtype)) return bad("input/output pointer not aligned to its element size");
+  if (!dl::is_aligned(log_decay, 4) || !dl::is_aligned(state, 4) || !dl::is_aligned(new_state, 4) ||
+      !dl::is_aligned(dev_err, 4))
+    return bad("fp32 pointer not 4-byte aligned");
+  ScanArgs a{};
+  a.x = x;
+  a.log_decay = log_decay;
+  a.h0 = state;
+  a.h_last = new_state;
+  a.h = h;
+  a.slot_idx = slot_idx;
+  a.err = dev_err;
+  a.slots = slots;
+  a.C = C;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int vec = vec_of(C, in_dtype, {x, h}, {log_decay, state, new_state});
+  const cudaError_t e = in_dtype == DL_BF16
+                            ? (vec == 2 ? launch_step<__nv_bfloat16, 2>(a, rows, st) : launch_step<__nv_bfloat16, 1>(a, rows, st))
+                            : (vec == 2 ? launch_step<float, 2>(a, rows, st) : launch_step<float, 1>(a, rows, st));
+  return e == cudaSuccess ? DL_OK : dl::launch_failed(e, "scan step launch");
+}
+
+}  // extern "C"

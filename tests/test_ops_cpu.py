@@ -1,0 +1,99 @@
+"""Refusals of the stateless operators: the C ABI rejects bad arguments before any CUDA call, the Python layer turns
+wrong shapes, types, layouts and devices into ValueError.  No GPU is touched."""
+import ctypes
+
+import pytest
+import torch
+
+from recurrent_state_update_deltalog_b200 import _native as N
+from recurrent_state_update_deltalog_b200.build import build
+
+ARG, UNSUPPORTED = -1, -2
+P, ODD = ctypes.c_void_p(64), ctypes.c_void_p(65)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build()
+    return N.load()
+
+
+def scan_args(**over):
+    a = dict(slot_idx=None, slots=2, rows=2, cu=None, total=8, C=4, dtype=1, x=P, d=P, h0=None, h_last=None, h=P,
+             ckpt=None, err=None)
+    a.update(over)
+    return list(a.values()) + [None]
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(dtype=2), ARG), (dict(C=0), ARG), (dict(C=(1 << 24) + 1), ARG), (dict(rows=-1), ARG), (dict(total=-8), ARG),
+    (dict(rows=65536, slots=65536, total=65536), UNSUPPORTED), (dict(rows=0, total=8), ARG), (dict(total=9), ARG),
+    (dict(slots=1), ARG), (dict(slot_idx=P, slots=0), ARG), (dict(x=None), ARG), (dict(d=None), ARG), (dict(h=None), ARG),
+    (dict(x=ODD), ARG), (dict(h=ODD), ARG), (dict(d=ODD), ARG), (dict(h0=ODD), ARG), (dict(ckpt=ODD), ARG),
+    (dict(err=ODD), ARG), (dict(slot_idx=ODD), ARG), (dict(cu=ODD), ARG), (dict(cu=P, total=1 << 31), UNSUPPORTED),
+])
+def test_scan_refusals(lib, over, status):
+    assert lib.dl_scan(*scan_args(**over)) == status
+    assert lib.dl_last_error()
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(dtype=-1), ARG), (dict(C=0), ARG), (dict(total=7), ARG), (dict(ckpt=None), ARG), (dict(dh=None), ARG),
+    (dict(dx=None), ARG), (dict(dld=None), ARG), (dict(dh=ODD), ARG), (dict(dx=ODD), ARG), (dict(dh0=ODD), ARG),
+    (dict(dh_last=ODD), ARG),
+])
+def test_scan_backward_refusals(lib, over, status):
+    a = dict(rows=2, cu=None, total=8, C=4, dtype=1, x=P, d=P, ckpt=P, dh=P, dh_last=None, dx=P, dld=P, dh0=None, err=None)
+    a.update(over)
+    assert lib.dl_scan_backward(*a.values(), None) == status
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(dtype=5), ARG), (dict(C=-4), ARG), (dict(slots=1), ARG), (dict(state=None), ARG), (dict(new=None), ARG),
+    (dict(h=None), ARG), (dict(state=ODD), ARG), (dict(rows=65536, slots=1 << 17), UNSUPPORTED),
+])
+def test_scan_step_refusals(lib, over, status):
+    a = dict(slot_idx=None, slots=2, rows=2, C=4, dtype=0, x=P, d=P, state=P, new=P, h=P, err=None)
+    a.update(over)
+    assert lib.dl_scan_step(*a.values(), None) == status
+
+
+def test_scan_without_rows_is_a_no_op(lib):
+    assert lib.dl_scan(*scan_args(rows=0, total=0, x=None, d=None, h=None)) == 0
+    assert lib.dl_scan_backward(0, None, 0, 4, 1, *[None] * 10) == 0
+    assert lib.dl_scan_step(None, 1, 0, 4, 1, *[None] * 7) == 0
+
+
+def test_scan_python_refusals():
+    from recurrent_state_update_deltalog_b200 import (gated_scan, gated_scan_backward, gated_scan_forward,
+                                                      gated_scan_prefill, gated_scan_step)
+    x, d = torch.zeros(2, 3, 4), torch.zeros(2, 3, 4)
+    x2, d2, pool = x[0].contiguous(), d[0].contiguous(), torch.zeros(5, 4)
+    cu = torch.zeros(3, dtype=torch.int32)
+    for bad, match in [
+        (lambda: gated_scan(x, d), "CUDA device"),
+        (lambda: gated_scan(x.half(), d), "bfloat16"),
+        (lambda: gated_scan(x, d.bfloat16()), "log_decay"),
+        (lambda: gated_scan(x, d[:, :2]), "log_decay"),
+        (lambda: gated_scan(x.transpose(0, 1), d.transpose(0, 1)), "contiguous"),
+        (lambda: gated_scan(x2, d2), "cu_seqlens"),
+        (lambda: gated_scan(x, d, cu_seqlens=cu), "total, C"),
+        (lambda: gated_scan(x2, d2, cu_seqlens=cu.long()), "cu_seqlens"),
+        (lambda: gated_scan(x2, d2, cu_seqlens=cu[:0]), "offsets"),
+        (lambda: gated_scan(x, d, h0=torch.zeros(3, 4)), "h0"),
+        (lambda: gated_scan(x, d, h0=torch.zeros(2, 4).bfloat16()), "h0"),
+        (lambda: gated_scan_forward(x, d, err=torch.zeros(1)), "err"),
+        (lambda: gated_scan_backward(x, d, torch.zeros(1, 4), d), "ckpt"),
+        (lambda: gated_scan_backward(x, d, torch.zeros(2, 4), d2), "dh"),
+        (lambda: gated_scan_prefill(x2, d2, pool, None), "cu_seqlens"),
+        (lambda: gated_scan_prefill(x2, d2, pool[:1], cu), "slots"),
+        (lambda: gated_scan_prefill(x2, d2, pool[:, :2], cu), "state"),
+        (lambda: gated_scan_prefill(x2, d2, pool, cu, slot_idx=cu), "slot_idx"),
+        (lambda: gated_scan_step(x2, d2, pool, slot_idx=cu[:2]), "slot_idx"),
+        (lambda: gated_scan_step(x2, d2, pool, new_state=pool[:4]), "new_state"),
+        (lambda: gated_scan_step(x2, d2, pool, out=x2[:2]), "out"),
+        (lambda: gated_scan_step(x2, d2, pool.double()), "state"),
+        (lambda: gated_scan_step(x2, d2, pool), "CUDA device"),
+    ]:
+        with pytest.raises(ValueError, match=match):
+            bad()
