@@ -446,6 +446,42 @@ int dl_scan_step(const int* slot_idx, int slots, int rows, int C, int in_dtype, 
                  const float* log_decay, const float* state, float* new_state, void* h,
                  int* dev_err, void* stream);
 
+/* Norms before and after a block, fused with its gate and residual scale.
+ * Per row of D channels, with every part but y optional (NULL):
+ *     u = y;  u = u / sqrt(mean(u^2) + eps) * post_weight  (mean over each of
+ *     `groups` groups of D / groups channels);  u = u * silu(gate);
+ *     out = residual + scale * u;
+ *     normed = out / sqrt(mean(out^2) + eps) * pre_weight  (mean over D).
+ * groups = H and a gate give the gated norm of each head's output o [rows][H]
+ * [d_v] of dl_step; groups = 1 the joint between two blocks.
+ *   y, gate, residual, out, normed  typed [rows][D];
+ *   post_weight float [D / groups], scale, pre_weight float [D] (both need
+ *   groups = 1, DL_ERR_UNSUPPORTED otherwise);
+ *   out may be NULL with a pre_weight; normed goes with pre_weight alone.
+ * out and normed may be y, gate or residual (not each other).  Rows skipped by
+ * the slot map (of `slots` slots) are not written.  D / groups <= 8192.
+ * Everything between the inputs and the outputs is fp32: normed is formed
+ * from the unrounded out. */
+int dl_block_norm(const int* slot_idx, int slots, int rows, int D, int groups, int in_dtype,
+                  const void* y, const float* post_weight, const void* gate, const float* scale,
+                  const void* residual, const float* pre_weight, float eps, void* out, void* normed,
+                  void* stream);
+
+/* Backward pass of dl_block_norm (no slot map) from dout and dnormed (typed
+ * [rows][D], each NULL for zeros): dy, dgate, dresidual typed [rows][D],
+ * dpost float [D / groups], dscale, dpre float [D], each NULL if not wanted.
+ * No output may overlap another tensor of the call.  The parameter gradients
+ * sum over rows (and groups) in fp32 in a fixed order, through `workspace`: a
+ * 4-byte aligned buffer of dl_block_norm_workspace bytes, not to be used by
+ * two calls that may overlap; NULL if none of the three is wanted. */
+int dl_block_norm_workspace(int rows, int D, int groups, size_t* bytes);
+int dl_block_norm_backward(int rows, int D, int groups, int in_dtype, const void* y,
+                           const float* post_weight, const void* gate, const float* scale,
+                           const void* residual, const float* pre_weight, float eps,
+                           const void* dout, const void* dnormed, void* dy, void* dgate,
+                           void* dresidual, float* dpost, float* dscale, float* dpre,
+                           void* workspace, void* stream);
+
 /* Bits of the device error word. */
 enum dl_device_error {
   DL_DEVERR_WAIT_TIMEOUT = 1,  /* a bounded wait gave up (a log copy in a step: that unit wrote

@@ -75,6 +75,23 @@ __device__ __forceinline__ void store_stream(T* p, const Pack<T, N>& r) {
   }
 }
 
+__device__ __forceinline__ void raise_error(int* err, int bit) {
+  if (err) atomicOr(err, bit);
+}
+
+// Slot of row r under a slot map (null: the row itself); -1 for a row to skip,
+// an index past the pool being reported by the thread with `tell`.
+__device__ __forceinline__ int row_slot(const int* slot_idx, int slots, int r, int* err, bool tell) {
+  if (!slot_idx) return r;
+  const int raw = __ldg(slot_idx + r);
+  if (raw < 0 || (raw & DL_SLOT_HOLD)) return -1;
+  if (raw >= slots) {
+    if (tell) raise_error(err, DL_DEVERR_SLOT_INDEX);
+    return -1;
+  }
+  return raw;
+}
+
 // Thread-block cluster: this CTA's rank, a barrier of all its CTAs' threads
 // (releases and acquires shared memory writes across the cluster), and a store
 // into the same shared memory location of CTA `rank`.

@@ -48,10 +48,6 @@ struct ScanArgs {
   int C;
 };
 
-__device__ __forceinline__ void raise_error(int* err, int bit) {
-  if (err) atomicOr(err, bit);
-}
-
 // Tokens of row r; false (row skipped, error raised by one thread) for a range
 // outside [0, total].
 __device__ __forceinline__ bool scan_row(const ScanArgs& a, int r, bool tell, long long* t0, long long* n) {
@@ -68,18 +64,6 @@ __device__ __forceinline__ bool scan_row(const ScanArgs& a, int r, bool tell, lo
     return false;
   }
   return true;
-}
-
-// Slot of row r; -1 for a row to skip.
-__device__ __forceinline__ int scan_slot(const ScanArgs& a, int r, bool tell) {
-  if (!a.slot_idx) return r;
-  const int raw = __ldg(a.slot_idx + r);
-  if (raw < 0 || (raw & DL_SLOT_HOLD)) return -1;
-  if (raw >= a.slots) {
-    if (tell) raise_error(a.err, DL_DEVERR_SLOT_INDEX);
-    return -1;
-  }
-  return raw;
 }
 
 // One warp's tokens [t, t + kScanTok) of a row of n tokens starting at token
@@ -122,7 +106,7 @@ __global__ void __launch_bounds__(kScanWarps * 32) scan_kernel(ScanArgs a, int N
   const int r = blockIdx.y;
   const bool tell = blockIdx.x == 0 && threadIdx.x == 0;
   long long t0, n;
-  const int slot = scan_slot(a, r, tell);
+  const int slot = row_slot(a.slot_idx, a.slots, r, a.err, tell);
   if (slot < 0) return;  // the same for every CTA of the cluster
   if (!scan_row(a, r, tell, &t0, &n)) return;
   const bool live = c < a.C;  // C % V == 0
@@ -428,7 +412,7 @@ template <typename TX, int V>
 __global__ void __launch_bounds__(128) scan_step_kernel(ScanArgs a) {
   const int r = blockIdx.y;
   const int c = (static_cast<int>(blockIdx.x) * 128 + static_cast<int>(threadIdx.x)) * V;
-  const int slot = scan_slot(a, r, blockIdx.x == 0 && threadIdx.x == 0);
+  const int slot = row_slot(a.slot_idx, a.slots, r, a.err, blockIdx.x == 0 && threadIdx.x == 0);
   if (slot < 0 || c >= a.C) return;
   const long long in = static_cast<long long>(r) * a.C + c, st = static_cast<long long>(slot) * a.C + c;
   const auto x = load_stream<TX, V>(static_cast<const TX*>(a.x) + in);

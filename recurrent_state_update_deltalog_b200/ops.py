@@ -17,6 +17,7 @@ on another stream than the captured one.
 """
 from __future__ import annotations
 
+import ctypes
 import functools
 
 import torch
@@ -29,17 +30,22 @@ _F32, _I32 = torch.float32, torch.int32
 
 def _placed(fn):
     """Run ``fn`` with its first tensor's device current, on ``stream`` if given."""
+    first = fn.__code__.co_varnames[0]
+
     @functools.wraps(fn)
-    def call(x, *args, stream=None, **kw):
+    def call(*args, stream=None, **kw):
+        x = args[0] if args else kw.get(first)
+        if not isinstance(x, torch.Tensor):
+            raise ValueError(f"{first} must be a tensor")
         if stream is not None:
             if stream.device != x.device:
-                raise ValueError(f"stream belongs to {stream.device}, the tensors to {x.device}")
+                raise ValueError(f"stream belongs to {stream.device}, {first} to {x.device}")
             with torch.cuda.stream(stream):
-                return fn(x, *args, **kw)
+                return fn(*args, **kw)
         if x.is_cuda and x.device.index != torch.cuda.current_device():
             with torch.cuda.device(x.device):
-                return fn(x, *args, **kw)
-        return fn(x, *args, **kw)
+                return fn(*args, **kw)
+        return fn(*args, **kw)
     return call
 
 
@@ -255,3 +261,112 @@ def gated_scan_step(x, log_decay, state, slot_idx=None, new_state=None, out=None
     N.call("dl_scan_step", _ptr(slot_idx), state.shape[0], rows, C, dt, _ptr(x), _ptr(log_decay), _ptr(state),
            _ptr(state if new_state is None else new_state), _ptr(h), _ptr(err), _stream(x))
     return h
+
+
+# -- norms around a block ----------------------------------------------------------------------
+
+def _norm_check(y, post_weight, gate, scale, residual, pre_weight, groups):
+    dt = _check_first("y", y, range(1, 9))
+    groups = int(groups)
+    if groups > 1 and y.dim() >= 3 and y.shape[-2] == groups:      # [..., H, d]: the groups are a dimension
+        D = groups * y.shape[-1]
+    else:
+        D = y.shape[-1]
+    if groups < 1 or D < 1 or D % groups:
+        raise ValueError(f"the last dimension ({D}) must be a positive multiple of groups ({groups})")
+    for name, t in (("gate", gate), ("residual", residual)):
+        if t is not None:
+            _check(name, t, y.shape, y.dtype, y.device)
+    for name, t, n in (("post_weight", post_weight, D // groups), ("scale", scale, D), ("pre_weight", pre_weight, D)):
+        if t is not None:
+            _check(name, t, (n,), _F32, y.device)
+    return dt, y.numel() // D, D
+
+
+def _block_norm(y, post_weight, gate, scale, residual, pre_weight, groups, eps, slot_idx, slots, out, normed):
+    dt, rows, D = _norm_check(y, post_weight, gate, scale, residual, pre_weight, groups)
+    if slot_idx is not None:
+        _check_index("slot_idx", slot_idx, y.device, rows)
+    if normed is not None and pre_weight is None:
+        raise ValueError("normed_out goes with pre_weight")
+    for name, t in (("out", out), ("normed_out", normed)):
+        if t is not None:
+            _check(name, t, y.shape, y.dtype, y.device)
+    _check_cuda("y", y)
+    out = torch.empty_like(y) if out is None else out
+    if pre_weight is not None and normed is None:
+        normed = torch.empty_like(y)
+    N.call("dl_block_norm", _ptr(slot_idx), slots, rows, D, groups, dt, _ptr(y), _ptr(post_weight), _ptr(gate), _ptr(scale),
+           _ptr(residual), _ptr(pre_weight), eps, _ptr(out), _ptr(normed), _stream(y))
+    return out, normed
+
+
+@_placed
+def block_norm_backward(y, dout, dnormed=None, post_weight=None, gate=None, scale=None, residual=None, pre_weight=None,
+                        groups=1, eps=1e-6, need=(True,) * 6):
+    """Gradients of :func:`block_norm` for dout and dnormed (each None: zeros), in the
+    order y, post_weight, gate, scale, residual, pre_weight; None for absent parts and
+    where ``need`` says False."""
+    dt, rows, D = _norm_check(y, post_weight, gate, scale, residual, pre_weight, groups)
+    if dnormed is not None and pre_weight is None:
+        raise ValueError("dnormed goes with pre_weight")
+    for name, t in (("dout", dout), ("dnormed", dnormed)):
+        if t is not None:
+            _check(name, t, y.shape, y.dtype, y.device)
+    _check_cuda("y", y)
+    parts = (y, post_weight, gate, scale, residual, pre_weight)
+    grads = [torch.empty_like(t) if t is not None and k else None for t, k in zip(parts, need)]
+    dy, dpost, dgate, dscale, dres, dpre = grads
+    work = None
+    if dpost is not None or dscale is not None or dpre is not None:
+        nbytes = ctypes.c_size_t()
+        N.call("dl_block_norm_workspace", rows, D, groups, ctypes.byref(nbytes))
+        work = torch.empty(max(nbytes.value, 1), dtype=torch.uint8, device=y.device)
+    N.call("dl_block_norm_backward", rows, D, groups, dt, _ptr(y), _ptr(post_weight), _ptr(gate), _ptr(scale), _ptr(residual),
+           _ptr(pre_weight), eps, _ptr(dout), _ptr(dnormed), _ptr(dy), _ptr(dgate), _ptr(dres), _ptr(dpost), _ptr(dscale),
+           _ptr(dpre), _ptr(work), _stream(y))
+    return tuple(grads)
+
+
+class _BlockNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, y, post_weight, gate, scale, residual, pre_weight, groups, eps):
+        out, normed = _block_norm(y, post_weight, gate, scale, residual, pre_weight, groups, eps, None, 0, None, None)
+        ctx.save_for_backward(y, post_weight, gate, scale, residual, pre_weight)
+        ctx.groups, ctx.eps = groups, eps
+        ctx.set_materialize_grads(False)
+        return out if normed is None else (out, normed)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout, dnormed=None):
+        y, post_weight, gate, scale, residual, pre_weight = ctx.saved_tensors
+        grads = block_norm_backward(y, None if dout is None else dout.contiguous(),
+                                    None if dnormed is None else dnormed.contiguous(), post_weight, gate, scale,
+                                    residual, pre_weight, ctx.groups, ctx.eps, ctx.needs_input_grad[:6])
+        return (*grads, None, None)
+
+
+@_placed
+def block_norm(y, post_weight=None, gate=None, scale=None, residual=None, pre_weight=None, groups=1, eps=1e-6,
+               slot_idx=None, slots=None, out=None, normed_out=None):
+    """Norms after and before a block, with its gate, residual scale and residual.
+
+    u = RMSNorm(y) * post_weight (over ``groups`` groups of the last dimension), times
+    silu(gate), times scale; out = residual + u; normed = RMSNorm(out) * pre_weight.
+    Every part but y may be None.  y, gate, residual are bf16 or fp32 [..., D]; weights
+    fp32: post_weight [D / groups], scale and pre_weight [D] (groups = 1 only).  With
+    ``groups = H`` y may also be [..., H, d].  Returns out, or (out, normed) with a
+    pre_weight; differentiable in every part.
+
+    Serving (no gradients): ``out`` and ``normed_out`` may be y, gate or residual (in
+    place); with ``slot_idx`` (int32 [rows]) rows of negative, held or, given ``slots``,
+    too large slots are not written."""
+    parts = (y, post_weight, gate, scale, residual, pre_weight)
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in parts):
+        if slot_idx is not None or out is not None or normed_out is not None:
+            raise ValueError("slot_idx, out and normed_out are for calls without gradients")
+        return _BlockNorm.apply(*parts, int(groups), float(eps))
+    out, normed = _block_norm(*parts, int(groups), float(eps), slot_idx, 0x7fffffff if slots is None else int(slots), out,
+                              normed_out)
+    return out if normed is None else (out, normed)

@@ -97,3 +97,69 @@ def test_scan_python_refusals():
     ]:
         with pytest.raises(ValueError, match=match):
             bad()
+
+
+def norm_args(**over):
+    a = dict(slot_idx=None, slots=0, rows=2, D=8, groups=1, dtype=1, y=P, post=None, gate=None, scale=None, residual=None,
+             pre=None, eps=1e-6, out=P, normed=None)
+    a.update(over)
+    return list(a.values()) + [None]
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(dtype=3), ARG), (dict(rows=-1), ARG), (dict(D=0), ARG), (dict(groups=3), ARG), (dict(groups=0), ARG),
+    (dict(D=8193), UNSUPPORTED), (dict(D=8200, groups=1), UNSUPPORTED), (dict(groups=2, scale=P), UNSUPPORTED),
+    (dict(groups=2, pre=P, normed=P), UNSUPPORTED), (dict(eps=-1.0), ARG), (dict(eps=float("nan")), ARG), (dict(y=None), ARG),
+    (dict(out=None), ARG), (dict(pre=P), ARG), (dict(normed=P), ARG), (dict(y=ODD), ARG), (dict(out=ODD), ARG),
+    (dict(post=ODD), ARG), (dict(slot_idx=P, slots=0), ARG), (dict(slot_idx=ODD, slots=2), ARG),
+    (dict(rows=1 << 30, groups=4), UNSUPPORTED),
+])
+def test_norm_refusals(lib, over, status):
+    assert lib.dl_block_norm(*norm_args(**over)) == status
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(D=8193), UNSUPPORTED), (dict(y=None), ARG), (dict(dgate=P), ARG), (dict(dresidual=P), ARG), (dict(dpost=P), ARG),
+    (dict(dscale=P), ARG), (dict(dpre=P), ARG), (dict(dnormed=P), ARG), (dict(post=P, dpost=P), ARG), (dict(dy=ODD), ARG),
+    (dict(dout=ODD), ARG),
+])
+def test_norm_backward_refusals(lib, over, status):
+    a = dict(rows=2, D=8, groups=1, dtype=1, y=P, post=None, gate=None, scale=None, residual=None, pre=None, eps=1e-6,
+             dout=P, dnormed=None, dy=P, dgate=None, dresidual=None, dpost=None, dscale=None, dpre=None, work=None)
+    a.update(over)
+    assert lib.dl_block_norm_backward(*a.values(), None) == status
+
+
+def test_norm_workspace(lib):
+    n = ctypes.c_size_t()
+    assert lib.dl_block_norm_workspace(4, 64, 2, ctypes.byref(n)) == 0 and n.value == 8 * 3 * 32 * 4
+    assert lib.dl_block_norm_workspace(4, 64, 3, ctypes.byref(n)) == ARG
+    assert lib.dl_block_norm_workspace(4, 64, 2, None) == ARG
+    assert lib.dl_block_norm(*norm_args(rows=0, y=None, out=None)) == 0
+
+
+def test_norm_python_refusals():
+    from recurrent_state_update_deltalog_b200 import block_norm, block_norm_backward
+    y, w = torch.zeros(3, 8), torch.ones(8)
+    grad = y.clone().requires_grad_()
+    idx = torch.zeros(3, dtype=torch.int32)
+    for bad, match in [
+        (lambda: block_norm(y, w), "CUDA device"),
+        (lambda: block_norm(y.double(), w), "bfloat16"),
+        (lambda: block_norm(y, w[:4]), "post_weight"),
+        (lambda: block_norm(y, w.bfloat16()), "post_weight"),
+        (lambda: block_norm(y, w, groups=2), "post_weight"),
+        (lambda: block_norm(y, groups=3), "multiple"),
+        (lambda: block_norm(y.t(), w[:3]), "contiguous"),
+        (lambda: block_norm(y, gate=y[:2]), "gate"),
+        (lambda: block_norm(y, gate=y.bfloat16()), "gate"),
+        (lambda: block_norm(y, residual=torch.zeros(8, 3).t()), "residual"),
+        (lambda: block_norm(y, normed_out=y), "pre_weight"),
+        (lambda: block_norm(y, w, out=y[:2]), "out"),
+        (lambda: block_norm(y, w, slot_idx=idx[:2]), "slot_idx"),
+        (lambda: block_norm(grad, w, out=y), "without gradients"),
+        (lambda: block_norm_backward(y, y, dnormed=y), "pre_weight"),
+        (lambda: block_norm_backward(y, y[:2]), "dout"),
+    ]:
+        with pytest.raises(ValueError, match=match):
+            bad()
