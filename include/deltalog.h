@@ -482,6 +482,40 @@ int dl_block_norm_backward(int rows, int D, int groups, int in_dtype, const void
                            void* dresidual, float* dpost, float* dscale, float* dpre,
                            void* workspace, void* stream);
 
+/* Attention of one new token over a paged key-value cache, for the attention
+ * layers between recurrent ones.  Per row r on slot s, query head h of
+ * key-value head g = h / (Hq / Hkv), over positions j of
+ * [max(0, lens[s] - window), lens[s]) (window 0: all):
+ *     o_h = sum_j softmax_j(scale q_h . k_j) v_j;  no position: o_h = 0.
+ *   k_pages, v_pages  typed [num_pages][Hkv][page_size][d]: position j of slot
+ *               s is row j % page_size of page table[s][j / page_size];
+ *   table       device int32 [slots][max_pages], lens device int32 [slots];
+ *               lens counts the new token.  A row whose lens lies outside
+ *               [0, max_pages * page_size] is skipped (DL_DEVERR_SEQLEN); a
+ *               page id outside [0, num_pages) counts as absent positions
+ *               (DL_DEVERR_PAGE).  Entries past a row's length are not read;
+ *   q, out      typed [rows][Hq][d] (out may be q);
+ *   k, v        typed [rows][Hkv][d], the new token's, stored at position
+ *               lens[s] - 1 and used from here; both NULL: already stored.
+ * Hq a multiple of Hkv; d in {64, 128}; page_size a power of two; pointers of
+ * typed tensors 16-byte aligned.  The split over the length follows max_pages
+ * (or the window), so a table no wider than needed is fastest.  Scores and
+ * sums are fp32; with bf16 the weights enter their product with v as bf16. */
+int dl_paged_attention(const int* slot_idx, int slots, int rows, int Hq, int Hkv, int d, int in_dtype,
+                       int page_size, long long num_pages, int max_pages, const int* table,
+                       const int* lens, int window, float scale, const void* q, const void* k,
+                       const void* v, void* k_pages, void* v_pages, void* out, int* dev_err,
+                       void* stream);
+
+/* Copy prompts into the pages: tokens [cu_seqlens[r], cu_seqlens[r + 1]) of k
+ * and v (typed [total][Hkv][d]) to positions starts[s] + 0, 1, ... of row r's
+ * slot s (starts device int32 [slots], or NULL: 0).  A row whose range is
+ * invalid or passes max_pages * page_size is skipped (DL_DEVERR_SEQLEN). */
+int dl_paged_write(const int* slot_idx, int slots, int rows, const int* cu_seqlens, long long total,
+                   int Hkv, int d, int in_dtype, int page_size, long long num_pages, int max_pages,
+                   const int* table, const int* starts, const void* k, const void* v, void* k_pages,
+                   void* v_pages, int* dev_err, void* stream);
+
 /* Bits of the device error word. */
 enum dl_device_error {
   DL_DEVERR_WAIT_TIMEOUT = 1,  /* a bounded wait gave up (a log copy in a step: that unit wrote
@@ -490,7 +524,9 @@ enum dl_device_error {
                                   when the hardware did not finish work it was given within a
                                   second; treat the CUDA context as suspect afterwards */
   DL_DEVERR_SLOT_INDEX = 2,    /* a slot index >= B (indexed steps, dl_prefill) */
-  DL_DEVERR_SEQLEN = 4         /* a row's cu_seqlens range is invalid (dl_prefill, dl_scan) */
+  DL_DEVERR_SEQLEN = 4,        /* a row's cu_seqlens range or length is invalid (dl_prefill, dl_scan,
+                                  dl_paged_*) */
+  DL_DEVERR_PAGE = 8           /* a page id outside the cache (dl_paged_*) */
 };
 
 /* Read and clear the handle's device error word in one atomic step on

@@ -20,7 +20,7 @@ DL_PREFILL_ZERO_STATE = 1
 DL_STATIC_SCRATCH_BYTES = 16 << 20
 DL_SLOT_HOLD = 0x40000000
 DL_SCAN_CHUNK = 64
-DL_DEVERR_SLOT_INDEX, DL_DEVERR_SEQLEN = 2, 4
+DL_DEVERR_SLOT_INDEX, DL_DEVERR_SEQLEN, DL_DEVERR_PAGE = 2, 4, 8
 DL_OPT_STEP_KERNEL = 0
 DL_OPT_HOST_PREFETCH = 1
 DL_OPT_PDL = 2
@@ -67,6 +67,8 @@ SIGNATURES = {
     "dl_block_norm": (_I, [_P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, ctypes.c_float, _P, _P, _P]),
     "dl_block_norm_workspace": (_I, [_I, _I, _I, ctypes.POINTER(ctypes.c_size_t)]),
     "dl_block_norm_backward": (_I, [_I, _I, _I, _I, _P, _P, _P, _P, _P, _P, ctypes.c_float] + [_P] * 10),
+    "dl_paged_attention": (_I, [_P, _I, _I, _I, _I, _I, _I, _I, ctypes.c_longlong, _I, _P, _P, _I, ctypes.c_float] + [_P] * 8),
+    "dl_paged_write": (_I, [_P, _I, _I, _P, ctypes.c_longlong, _I, _I, _I, _I, ctypes.c_longlong, _I] + [_P] * 8),
     "dl_strerror": (ctypes.c_char_p, [_I]),
     "dl_last_error": (ctypes.c_char_p, []),
 }

@@ -1,8 +1,9 @@
 """Operators that stand beside the recurrent layers (marshalling only).
 
 ``gated_scan`` (with its gradient, its prompt and its single-token form) is the
-elementwise member of the recurrent family.  Every computation runs in the CUDA
-library; shapes, dtypes and devices are checked here, so that a caller's mistake
+elementwise member of the recurrent family; ``block_norm`` the norms, gate and
+residual around any block; ``paged_attention`` the decode step of attention layers
+between recurrent ones.  Every computation runs in the CUDA library; shapes, dtypes and devices are checked here, so that a caller's mistake
 becomes a Python exception before a pointer crosses the C ABI.
 
 Conventions.  Tensors are contiguous CUDA tensors of one device, which need not
@@ -100,7 +101,8 @@ def check_errors(err):
     bits = int(err.item())
     if bits:
         err.zero_()
-        names = {N.DL_DEVERR_SLOT_INDEX: "slot index past the pool", N.DL_DEVERR_SEQLEN: "invalid cu_seqlens range"}
+        names = {N.DL_DEVERR_SLOT_INDEX: "slot index past the pool", N.DL_DEVERR_SEQLEN: "invalid cu_seqlens range or length",
+                 N.DL_DEVERR_PAGE: "page id outside the cache"}
         raise N.DeltaLogError("check_errors", -5, ", ".join(v for k, v in names.items() if bits & k) or hex(bits))
 
 
@@ -370,3 +372,75 @@ def block_norm(y, post_weight=None, gate=None, scale=None, residual=None, pre_we
     out, normed = _block_norm(*parts, int(groups), float(eps), slot_idx, 0x7fffffff if slots is None else int(slots), out,
                               normed_out)
     return out if normed is None else (out, normed)
+
+
+# -- paged key-value cache -----------------------------------------------------------------------
+
+def _cache_check(x, k_pages, v_pages, block_table, heads):
+    """(num_pages, Hkv, page_size, d, slots, max_pages) of a cache for x [rows, heads, d]."""
+    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
+        raise ValueError("k_pages must be [num_pages, Hkv, page_size, d]")
+    num_pages, Hkv, page, d = k_pages.shape
+    _check("k_pages", k_pages, k_pages.shape, x.dtype, x.device)
+    _check("v_pages", v_pages, k_pages.shape, x.dtype, x.device)
+    if x.shape[2] != d or Hkv < 1 or x.shape[1] % Hkv or (heads and x.shape[1] != Hkv):
+        raise ValueError(f"heads {tuple(x.shape[1:])} do not fit a cache of {Hkv} heads of {d}")
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be [slots, max_pages]")
+    _check("block_table", block_table, block_table.shape, _I32, x.device)
+    return num_pages, Hkv, page, d, block_table.shape[0], block_table.shape[1]
+
+
+@_placed
+def paged_attention(q, k_pages, v_pages, block_table, lens, k=None, v=None, slot_idx=None, window=0, scale=None, out=None,
+                    err=None):
+    """Attention of one new token a row over a paged cache; returns o like q.
+
+    q [rows, Hq, d] bf16 or fp32 (d 64 or 128); k_pages, v_pages [num_pages, Hkv,
+    page_size, d] of the same type; block_table int32 [slots, max_pages]; lens int32
+    [slots], the new token included; row r runs on slot ``slot_idx[r]`` (default r;
+    negative or held: skipped, its output not written).  With k, v [rows, Hkv, d] the
+    new token is stored at position lens - 1 first.  ``window`` > 0 keeps the last
+    ``window`` positions.  scale defaults to d ** -0.5.  A slot of length 0 gives zeros."""
+    dt = _check_first("q", q, (3,))
+    num_pages, Hkv, page, d, slots, max_pages = _cache_check(q, k_pages, v_pages, block_table, False)
+    rows = q.shape[0]
+    _check_index("lens", lens, q.device, slots)
+    _check_slots(slot_idx, rows, slots, q.device)
+    if not 0 <= int(window) < 1 << 31:
+        raise ValueError("window must be 0 (none) or a positive 32-bit number")
+    if (k is None) != (v is None):
+        raise ValueError("k and v go together")
+    if k is not None:
+        _check("k", k, (rows, Hkv, d), q.dtype, q.device)
+        _check("v", v, (rows, Hkv, d), q.dtype, q.device)
+    if out is not None:
+        _check("out", out, q.shape, q.dtype, q.device)
+    _check_err(err, q.device)
+    _check_cuda("q", q)
+    out = torch.empty_like(q) if out is None else out
+    N.call("dl_paged_attention", _ptr(slot_idx), slots, rows, q.shape[1], Hkv, d, dt, page, num_pages, max_pages,
+           _ptr(block_table), _ptr(lens), int(window), d ** -0.5 if scale is None else float(scale), _ptr(q), _ptr(k), _ptr(v),
+           _ptr(k_pages), _ptr(v_pages), _ptr(out), _ptr(err), _stream(q))
+    return out
+
+
+@_placed
+def paged_write(k, v, k_pages, v_pages, block_table, cu_seqlens, starts=None, slot_idx=None, err=None):
+    """Copy packed prompts k, v [total, Hkv, d] into a paged cache: row r's tokens
+    [cu_seqlens[r], cu_seqlens[r + 1]) to positions starts[slot] + 0, 1, ... of its slot
+    (``starts`` int32 [slots], default 0; slots as in :func:`paged_attention`)."""
+    dt = _check_first("k", k, (3,))
+    _check("v", v, k.shape, k.dtype, k.device)
+    num_pages, Hkv, page, d, slots, max_pages = _cache_check(k, k_pages, v_pages, block_table, True)
+    _check_index("cu_seqlens", cu_seqlens, k.device)
+    rows = cu_seqlens.numel() - 1
+    if rows < 0:
+        raise ValueError("cu_seqlens must hold rows + 1 offsets")
+    if starts is not None:
+        _check_index("starts", starts, k.device, slots)
+    _check_slots(slot_idx, rows, slots, k.device)
+    _check_err(err, k.device)
+    _check_cuda("k", k)
+    N.call("dl_paged_write", _ptr(slot_idx), slots, rows, _ptr(cu_seqlens), k.shape[0], Hkv, d, dt, page, num_pages, max_pages,
+           _ptr(block_table), _ptr(starts), _ptr(k), _ptr(v), _ptr(k_pages), _ptr(v_pages), _ptr(err), _stream(k))

@@ -163,3 +163,69 @@ def test_norm_python_refusals():
     ]:
         with pytest.raises(ValueError, match=match):
             bad()
+
+
+def paged_args(**over):
+    a = dict(slot_idx=None, slots=2, rows=2, Hq=4, Hkv=2, d=64, dtype=1, page=16, pages=8, max_pages=4, table=P, lens=P,
+             window=0, scale=0.1, q=P, k=None, v=None, kp=P, vp=P, out=P, err=None)
+    a.update(over)
+    return list(a.values()) + [None]
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(dtype=2), ARG), (dict(d=96), UNSUPPORTED), (dict(d=256), UNSUPPORTED), (dict(rows=-1), ARG), (dict(Hkv=0), ARG),
+    (dict(Hq=5), ARG), (dict(Hq=0), ARG), (dict(page=0), UNSUPPORTED), (dict(page=12), UNSUPPORTED),
+    (dict(page=1 << 21), UNSUPPORTED), (dict(pages=-1), ARG), (dict(pages=1 << 31), UNSUPPORTED), (dict(max_pages=-1), ARG),
+    (dict(max_pages=1 << 28), UNSUPPORTED), (dict(slots=1), ARG), (dict(slot_idx=P, slots=0), ARG),
+    (dict(rows=65536, slots=65536), UNSUPPORTED), (dict(window=-1), ARG), (dict(scale=float("nan")), ARG),
+    (dict(scale=float("inf")), ARG), (dict(table=None), ARG), (dict(lens=None), ARG), (dict(q=None), ARG), (dict(out=None), ARG),
+    (dict(kp=None), ARG), (dict(k=P), ARG), (dict(v=P), ARG), (dict(q=ctypes.c_void_p(72)), ARG), (dict(lens=ODD), ARG),
+    (dict(table=ODD), ARG),
+])
+def test_paged_refusals(lib, over, status):
+    assert lib.dl_paged_attention(*paged_args(**over)) == status
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(total=-1), ARG), (dict(total=1 << 31), ARG), (dict(cu=None), ARG), (dict(k=None), ARG), (dict(vp=None), ARG),
+    (dict(k=ctypes.c_void_p(72)), ARG), (dict(starts=ODD), ARG), (dict(page=3), UNSUPPORTED), (dict(d=32), UNSUPPORTED),
+])
+def test_paged_write_refusals(lib, over, status):
+    a = dict(slot_idx=None, slots=2, rows=2, cu=P, total=4, Hkv=2, d=64, dtype=1, page=16, pages=8, max_pages=4, table=P,
+             starts=None, k=P, v=P, kp=P, vp=P, err=None)
+    a.update(over)
+    assert lib.dl_paged_write(*a.values(), None) == status
+
+
+def test_paged_without_rows_is_a_no_op(lib):
+    assert lib.dl_paged_attention(*paged_args(rows=0, q=None, out=None, lens=None)) == 0
+
+
+def test_paged_python_refusals():
+    from recurrent_state_update_deltalog_b200 import paged_attention, paged_write
+    q, kp, tb, ln = torch.zeros(2, 4, 64), torch.zeros(5, 2, 16, 64), torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    k, cu = torch.zeros(2, 2, 64), torch.zeros(3, dtype=torch.int32)
+    for bad, match in [
+        (lambda: paged_attention(q, kp, kp, tb, ln), "CUDA device"),
+        (lambda: paged_attention(q.half(), kp, kp, tb, ln), "bfloat16"),
+        (lambda: paged_attention(q[0], kp, kp, tb, ln), "dimensions"),
+        (lambda: paged_attention(q, kp.bfloat16(), kp, tb, ln), "k_pages"),
+        (lambda: paged_attention(q, kp, kp[:4], tb, ln), "v_pages"),
+        (lambda: paged_attention(q[:, :3].contiguous(), kp, kp, tb, ln), "heads"),
+        (lambda: paged_attention(q, kp, kp, tb.long(), ln), "block_table"),
+        (lambda: paged_attention(q, kp, kp, tb[0], ln), "block_table"),
+        (lambda: paged_attention(q, kp, kp, tb, ln[:1]), "lens"),
+        (lambda: paged_attention(q, kp, kp, tb, ln, k=k), "together"),
+        (lambda: paged_attention(q, kp, kp, tb, ln, window=-1), "window"),
+        (lambda: paged_attention(q, kp, kp, tb, ln, window=1 << 32), "window"),
+        (lambda: paged_attention(q, kp, kp, tb, ln, k=k, v=k[:1]), "v: expected"),
+        (lambda: paged_attention(q, kp, kp, tb[:1], ln[:1]), "slots"),
+        (lambda: paged_attention(q, kp, kp, tb, ln, out=q[:1]), "out"),
+        (lambda: paged_write(k, k[:1], kp, kp, tb, cu), "v: expected"),
+        (lambda: paged_write(q, q, kp, kp, tb, cu), "heads"),
+        (lambda: paged_write(k, k, kp, kp, tb, cu[:0]), "offsets"),
+        (lambda: paged_write(k, k, kp, kp, tb, cu, starts=cu), "starts"),
+        (lambda: paged_write(k, k, kp, kp, tb, cu), "CUDA device"),
+    ]:
+        with pytest.raises(ValueError, match=match):
+            bad()
