@@ -9,25 +9,23 @@ namespace {
 
 using dl::ScanArgs;
 
+constexpr int kSms = 148;
+
 int bad(const char* msg) { return dl::record_error(DL_ERR_ARG, msg); }
 
-// Channels of one lane: two neighbours when every row of every tensor starts
-// on that many elements' alignment, else one.
-int vec_of(int C, int dtype, std::initializer_list<const void*> typed, std::initializer_list<const void*> f32) {
-  if (C % 2) return 1;
-  for (const void* p : typed)
-    if (p && !dl::is_aligned(p, dtype == DL_BF16 ? 4 : 8)) return 1;
-  for (const void* p : f32)
-    if (p && !dl::is_aligned(p, 8)) return 1;
-  return 2;
+// How the tensors' rows are aligned.
+int mode_of(int C, int dtype, std::initializer_list<const void*> tensors) {
+  for (const void* p : tensors)
+    if (!dl::is_aligned(p, 16)) return dl::NARROW;
+  return C % (dtype == DL_BF16 ? 8 : 4) ? dl::SHIFT : dl::WIDE;
 }
 
-// CTAs along time: enough that the launch has about four CTAs an SM, no more
-// than the sequences have chunks of 64 tokens on average.
+// CTAs along time: as many as it takes to give every SM one, if the sequences
+// have that many chunks of 64 tokens on average.
 int cluster_of(long long tiles, int rows, long long total) {
   const long long chunks = (total / rows + dl::kScanChunk - 1) / dl::kScanChunk;
   int n = 1;
-  while (n < 8 && 2 * n <= chunks && tiles * rows * n < 4 * 148) n *= 2;
+  while (n < 8 && 2 * n <= chunks && tiles * rows * n < kSms) n *= 2;
   return n;
 }
 
@@ -46,26 +44,47 @@ int check_common(int rows, long long total, int C, int dtype, const int* cu, con
 
 bool typed_ok(const void* p, int dtype) { return dl::is_aligned(p, dtype == DL_BF16 ? 2 : 4); }
 
-template <bool BACK, typename TX, int V>
+template <bool BACK, typename TX, int MODE, int PC, bool CLUSTER, int S>
+cudaError_t launch(const ScanArgs& a, int rows, int n, cudaStream_t st) {
+  const unsigned tiles = (a.C + 32 * PC - 1) / (32 * PC);
+  const auto kern = BACK ? dl::scan_backward_kernel<TX, MODE, PC, CLUSTER, S> : dl::scan_kernel<TX, MODE, PC, CLUSTER, S>;
+  const int smem = S * (BACK ? sizeof(dl::ScanBackStage<TX, MODE, PC>) : sizeof(dl::ScanStage<TX, MODE, PC>));
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return dl::launch_cluster(kern, dim3(tiles * n, rows), dl::kScanThreads, smem, st, n, a, n);
+}
+
+// Stages of the ring.  One where rows average no more than one chunk: nothing
+// is left to load ahead, and more CTAs share an SM.  Three while the launch has
+// up to three CTAs an SM, else two, for the occupancy.
+template <bool BACK, typename TX, int MODE>
 cudaError_t launch(const ScanArgs& a, int rows, cudaStream_t st) {
-  const long long tiles = (a.C + 32 * V - 1) / (32 * V);
-  const int n = cluster_of(tiles, rows, a.total);
-  const dim3 grid(static_cast<unsigned>(tiles * n), rows);
-  const int block = dl::kScanWarps * 32;
-  if constexpr (BACK) {
-    return n > 1 ? dl::launch_cluster(dl::scan_backward_kernel<TX, V, true>, grid, block, 0, st, n, a, n)
-                 : dl::launch_cluster(dl::scan_backward_kernel<TX, V, false>, grid, block, 0, st, 1, a, 1);
+  if constexpr (MODE == dl::NARROW) {
+    return launch<BACK, TX, MODE, 2, false, 1>(a, rows, 1, st);
   } else {
-    return n > 1 ? dl::launch_cluster(dl::scan_kernel<TX, V, true>, grid, block, 0, st, n, a, n)
-                 : dl::launch_cluster(dl::scan_kernel<TX, V, false>, grid, block, 0, st, 1, a, 1);
+    if (a.total / rows <= dl::kScanChunk) return launch<BACK, TX, MODE, 2, false, 1>(a, rows, 1, st);
+    const long long units = (a.C + 63) / 64 * static_cast<long long>(rows);
+    if (units < kSms) {
+      const int n = cluster_of((a.C + 31) / 32, rows, a.total);
+      return n > 1 ? launch<BACK, TX, MODE, 1, true, 3>(a, rows, n, st) : launch<BACK, TX, MODE, 1, false, 3>(a, rows, 1, st);
+    }
+    return units <= 3 * kSms ? launch<BACK, TX, MODE, 2, false, 3>(a, rows, 1, st)
+                             : launch<BACK, TX, MODE, 2, false, 2>(a, rows, 1, st);
+  }
+}
+
+template <bool BACK, typename TX>
+cudaError_t launch(const ScanArgs& a, int rows, int mode, cudaStream_t st) {
+  switch (mode) {
+    case dl::WIDE: return launch<BACK, TX, dl::WIDE>(a, rows, st);
+    case dl::SHIFT: return launch<BACK, TX, dl::SHIFT>(a, rows, st);
+    default: return launch<BACK, TX, dl::NARROW>(a, rows, st);
   }
 }
 
 template <bool BACK>
-cudaError_t launch(const ScanArgs& a, int rows, int dtype, int vec, cudaStream_t st) {
-  if (dtype == DL_BF16)
-    return vec == 2 ? launch<BACK, __nv_bfloat16, 2>(a, rows, st) : launch<BACK, __nv_bfloat16, 1>(a, rows, st);
-  return vec == 2 ? launch<BACK, float, 2>(a, rows, st) : launch<BACK, float, 1>(a, rows, st);
+cudaError_t launch(const ScanArgs& a, int rows, int dtype, int mode, cudaStream_t st) {
+  return dtype == DL_BF16 ? launch<BACK, __nv_bfloat16>(a, rows, mode, st) : launch<BACK, float>(a, rows, mode, st);
 }
 
 template <typename TX, int V>
@@ -105,7 +124,7 @@ int dl_scan(const int* slot_idx, int slots, int rows, const int* cu_seqlens, lon
   a.len = total / rows;
   a.slots = slots;
   a.C = C;
-  const cudaError_t e = launch<false>(a, rows, in_dtype, vec_of(C, in_dtype, {x, h}, {log_decay}),
+  const cudaError_t e = launch<false>(a, rows, in_dtype, mode_of(C, in_dtype, {x, h, log_decay}),
                                       static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? DL_OK : dl::launch_failed(e, "scan launch");
 }
@@ -137,7 +156,7 @@ int dl_scan_backward(int rows, const int* cu_seqlens, long long total, int C, in
   a.len = total / rows;
   a.slots = rows;
   a.C = C;
-  const cudaError_t e = launch<true>(a, rows, in_dtype, vec_of(C, in_dtype, {x, dh, dx}, {log_decay, dlog_decay}),
+  const cudaError_t e = launch<true>(a, rows, in_dtype, mode_of(C, in_dtype, {x, dh, dx, log_decay, dlog_decay}),
                                      static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? DL_OK : dl::launch_failed(e, "scan backward launch");
 }
@@ -164,7 +183,7 @@ int dl_scan_step(const int* slot_idx, int slots, int rows, int C, int in_dtype, 
   a.slots = slots;
   a.C = C;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int vec = vec_of(C, in_dtype, {x, h}, {log_decay, state, new_state});
+  const int vec = mode_of(C, in_dtype, {x, h, log_decay, state, new_state}) == dl::WIDE ? 2 : 1;
   const cudaError_t e = in_dtype == DL_BF16
                             ? (vec == 2 ? launch_step<__nv_bfloat16, 2>(a, rows, st) : launch_step<__nv_bfloat16, 1>(a, rows, st))
                             : (vec == 2 ? launch_step<float, 2>(a, rows, st) : launch_step<float, 1>(a, rows, st));

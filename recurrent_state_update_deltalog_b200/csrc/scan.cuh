@@ -8,13 +8,17 @@
 // second pass over the same registers produces every h_t from the true state
 // before the run.  The inputs are read once.
 //
-// Bound: memory (2 flops for 8 bytes an element with bf16 x and h).  Layout: a
-// CTA of 8 warps holds a chunk of 64 tokens by 32 * V channels, 8 tokens a
-// warp, V neighbouring channels a lane, all loads of a chunk in flight at
-// once.  Chunks of one sequence run in the CTAs of a cluster side by side: the
-// warps of a CTA exchange their (A, b) through shared memory, the CTAs of the
-// cluster through distributed shared memory, and the cluster then walks the
-// sequence N chunks at a time with the running state in registers.  No global
+// Bound: memory (2 flops for 8 bytes an element with bf16 x and h), with the
+// instruction rate close behind: an SM is fed 3 elements a clock.  So tiles of
+// 64 tokens by 64 channels travel by cp.async into a ring of shared memory
+// stages; addresses and bounds are paid once per 16 bytes, and what lies
+// outside the sequence arrives as zeros, which are the identity (log decay 0,
+// x 0).  A CTA of 4 warps takes 16 tokens a warp, two channels a lane, from
+// shared memory to registers once, and walks its sequence with the running
+// state in registers; its warps exchange their (A, b) through shared memory.
+// Where sequences and channels are too few to fill the GPU, the chunks of a
+// sequence run in the CTAs of a cluster side by side (one channel a lane), and
+// the CTAs exchange theirs through distributed shared memory.  No global
 // flags, no atomics: results do not depend on the order in which CTAs run.
 #pragma once
 
@@ -22,9 +26,10 @@
 
 namespace dl {
 
-constexpr int kScanWarps = 8;                      // warps of a CTA, consecutive in time
-constexpr int kScanTok = 8;                        // tokens a warp holds in registers
+constexpr int kScanWarps = 4;                      // warps of a CTA, consecutive in time
+constexpr int kScanTok = 16;                       // tokens of a warp, in registers
 constexpr int kScanChunk = kScanWarps * kScanTok;  // tokens of a CTA
+constexpr int kScanThreads = kScanWarps * 32;
 static_assert(kScanChunk == DL_SCAN_CHUNK, "checkpoint interval of the interface");
 
 struct ScanArgs {
@@ -66,168 +71,307 @@ __device__ __forceinline__ bool scan_row(const ScanArgs& a, int r, bool tell, lo
   return true;
 }
 
-// One warp's tokens [t, t + kScanTok) of a row of n tokens starting at token
-// t0, V channels from c, as loaded.  Tokens past the row read as the identity
-// (log decay 0, x 0).
-template <typename TX, int V>
-struct ScanTile {
-  Pack<TX, V> x[kScanTok];
-  Pack<float, V> d[kScanTok];
+// exp(x) for x <= 0 as 2^(x log2 e): off by 2^-22 of itself and 1.5 * 2^-24 |x|
+// of itself from the rounded product, which no state notices, since a decay
+// forgets e^x of what came before.
+__device__ __forceinline__ float decay_of(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+  return y;
+}
 
-  __device__ __forceinline__ void load(const ScanArgs& a, long long t0, long long t, long long n, int c, bool live) {
-    const long long base = (t0 + t) * a.C + c;
-    const TX* px = static_cast<const TX*>(a.x) + base;
-    const float* pd = a.log_decay + base;
+// How tiles travel, by the alignment of the tensors' rows:
+//   WIDE    every row starts on 16 bytes: 16-byte copies;
+//   SHIFT   only the tensors do: 16-byte copies of the aligned units that
+//           cover a row's channels, read from shared memory at the row's own
+//           shift;
+//   NARROW  neither: element by element, through registers.
+// With WIDE a lane takes neighbouring channels, else channels l and l + 32, so
+// that its warp's element-wise accesses are contiguous.
+enum { WIDE = 0, SHIFT = 1, NARROW = 2 };
+
+// cp.async of 16 bytes of which the first `bytes` are read and the rest zeros.
+__device__ __forceinline__ void copy_async16(void* dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(gmem_u64(src)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// 64 tokens by 32 * PC channels of one tensor in shared memory.
+template <typename T, int MODE, int PC>
+struct alignas(16) ScanTile {
+  static constexpr int V = 16 / sizeof(T);  // elements of a 16-byte unit
+  static constexpr int CH = 32 * PC;
+  static constexpr int P = CH + (MODE == SHIFT ? V : 0);
+  T v[kScanChunk][P];
+
+  // Starts bringing tokens [t, t + 64) of a row of n tokens (token t0 of the
+  // packed tensor p [total][C] its first), channels [c0, c0 + CH).  Tokens
+  // outside the row read as zeros; channels past C as zeros or as whatever
+  // follows them in the tensor, and nobody stores what comes of them.
+  __device__ __forceinline__ void load(const T* p, long long t0, long long t, long long n, int c0, int C, long long total) {
+    const int left = static_cast<int>(n - t < kScanChunk ? n - t : kScanChunk);  // may be negative
+    if constexpr (MODE == WIDE) {
+      constexpr int PER = CH / V, STEP = kScanThreads / PER;  // copies a token, tokens a pass
+      const int tok = threadIdx.x / PER, c = (threadIdx.x % PER) * V;
+      const bool in = c0 + c < C;
+      const T* src = p + (t0 + t + tok) * C + c0 + c;
 #pragma unroll
-    for (int i = 0; i < kScanTok; ++i) {
-      if (live && t + i < n) {
-        x[i] = load_stream<TX, V>(px + static_cast<long long>(i) * a.C);
-        d[i] = load_stream<float, V>(pd + static_cast<long long>(i) * a.C);
-      } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          x[i].v[j] = from_f32<TX>(0.f);
-          d[i].v[j] = 0.f;
-        }
+      for (int i = 0; i < kScanChunk / STEP; ++i) {
+        const bool live = in && tok + i * STEP < left;
+        copy_async16(&v[tok + i * STEP][c], live ? src : p, live ? 16 : 0);
+        src += static_cast<long long>(STEP) * C;
       }
+    } else if constexpr (MODE == SHIFT) {
+      // CH / V units cover CH elements from an aligned start; one more, which a
+      // second pass brings for all tokens, covers them from any
+      constexpr int PER = CH / V, STEP = kScanThreads / PER;
+      const int width = C - c0 < CH ? C - c0 : CH;
+      const bool last = t0 + t + kScanChunk >= total;  // the tensor may end inside a unit
+      auto unit = [&](int tok, int u) {
+        const long long e = (t0 + t + tok) * C + c0, from = (e & -V) + u * V;  // unit's first element
+        const bool live = tok < left && from < e + width;
+        int bytes = live ? 16 : 0;
+        if (last && live && total * C - from < V) bytes = static_cast<int>((total * C - from) * sizeof(T));
+        copy_async16(&v[tok][u * V], live ? p + from : p, bytes);
+      };
+#pragma unroll
+      for (int i = 0; i < kScanChunk / STEP; ++i) unit(threadIdx.x / PER + i * STEP, threadIdx.x % PER);
+      if (threadIdx.x < kScanChunk) unit(threadIdx.x, PER);
+    } else {
+      const int tok = threadIdx.x / CH, c = threadIdx.x % CH;
+      constexpr int STEP = kScanThreads / CH;
+      const T* const src = p + (t0 + t + tok) * C + c0 + c;
+#pragma unroll 8
+      for (int i = 0; i < kScanChunk / STEP; ++i)
+        v[tok + i * STEP][c] = c0 + c < C && tok + i * STEP < left ? src[static_cast<long long>(i) * STEP * C] : from_f32<T>(0.f);
+    }
+  }
+
+  // A lane's channels of token `tok`; `first`: low bits of the tile's first
+  // element's index in the tensor.
+  __device__ __forceinline__ Pack<T, PC> get(int tok, int lane, unsigned first, int C) const {
+    if constexpr (MODE == WIDE) return *reinterpret_cast<const Pack<T, PC>*>(&v[tok][PC * lane]);
+    const int at = lane + (MODE == SHIFT ? (first + static_cast<unsigned>(tok) * C) % V : 0);
+    Pack<T, PC> r;
+#pragma unroll
+    for (int j = 0; j < PC; ++j) r.v[j] = v[tok][at + 32 * j];
+    return r;
+  }
+};
+
+template <typename TX, int MODE, int PC>
+struct ScanStage {
+  ScanTile<float, MODE, PC> d;
+  ScanTile<TX, MODE, PC> x;
+};
+template <typename TX, int MODE, int PC>
+struct ScanBackStage {
+  ScanTile<float, MODE, PC> d;
+  ScanTile<TX, MODE, PC> x, g;
+};
+
+// A lane's channels in a row of the tensors: element j lies `step(j)` after p.
+template <int MODE>
+__device__ __forceinline__ constexpr int ch_step(int j) {
+  return MODE == WIDE ? j : 32 * j;
+}
+template <int MODE, int PC>
+__device__ __forceinline__ void load_row(float (&v)[PC], const float* p, const bool (&live)[PC]) {
+#pragma unroll
+  for (int j = 0; j < PC; ++j) v[j] = p && live[j] ? p[ch_step<MODE>(j)] : 0.f;
+}
+template <int MODE, int PC>
+__device__ __forceinline__ void store_row(float* p, const float (&v)[PC], const bool (&live)[PC]) {
+#pragma unroll
+  for (int j = 0; j < PC; ++j)
+    if (live[j]) p[ch_step<MODE>(j)] = v[j];
+}
+template <int MODE, typename T, int PC>
+__device__ __forceinline__ void store_out(T* p, const Pack<T, PC>& v, const bool (&live)[PC]) {
+  if constexpr (MODE == WIDE) {
+    if (live[0]) store_stream<T, PC>(p, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < PC; ++j)
+      if (live[j]) p[32 * j] = v.v[j];
+  }
+}
+
+// A map h -> A h + b of PC channels.
+template <int PC>
+struct alignas(8 * PC) ScanMap {
+  float A[PC], b[PC];
+  // What comes after this map, applied to its result.
+  __device__ __forceinline__ void then(const ScanMap& q) {
+#pragma unroll
+    for (int j = 0; j < PC; ++j) {
+      b[j] = fmaf(q.A[j], b[j], q.b[j]);
+      A[j] *= q.A[j];
+    }
+  }
+  __device__ __forceinline__ void apply(float (&h)[PC]) const {
+#pragma unroll
+    for (int j = 0; j < PC; ++j) h[j] = fmaf(A[j], h[j], b[j]);
+  }
+  __device__ __forceinline__ void identity() {
+#pragma unroll
+    for (int j = 0; j < PC; ++j) {
+      A[j] = 1.f;
+      b[j] = 0.f;
     }
   }
 };
 
-// Grid (channel tiles * N, rows), clusters of N along x.
-template <typename TX, int V, bool CLUSTER>
-__global__ void __launch_bounds__(kScanWarps * 32) scan_kernel(ScanArgs a, int N) {
-  __shared__ float2 part[2][kScanWarps][32 * V];  // each warp's (A, b)
-  __shared__ float2 tot[2][CLUSTER ? 16 : 1][32 * V];
+// The exchange of chunk totals in a cluster: at every step the last warp to
+// know its CTA's total sends it to all N CTAs (itself included), where the
+// bytes of N totals complete the step's mbarrier.  Two steps alternate between
+// two buffers: a CTA sends step s + 2 only after the others' step s + 1, which
+// they send only once all their warps have read step s.
+template <int PC>
+struct ScanExchange {
+  ScanMap<PC> tot[2][8][32];
+  uint64_t arrived[2];
+
+  __device__ __forceinline__ void start() {
+    if (threadIdx.x == 0) {
+      mbar_init(&arrived[0], 1);
+      mbar_init(&arrived[1], 1);
+      fence_mbar_init();
+    }
+    cluster_sync();  // every CTA of the cluster runs, and its barriers stand, before it is written to
+  }
+  __device__ __forceinline__ void send(int s, int N, int rank, const ScanMap<PC>& m) {
+    const int lane = threadIdx.x % 32, buf = s & 1;
+    if (lane == 0) mbar_arrive_expect_tx(&arrived[buf], N * 32 * static_cast<int>(sizeof(m)));
+    for (int q = 0; q < N; ++q) {
+      const uint32_t to = remote_smem(&tot[buf][rank][lane], q), bar = remote_smem(&arrived[buf], q);
+      if constexpr (PC == 2) send_remote(to, bar, make_float4(m.A[0], m.A[1], m.b[0], m.b[1]));
+      else send_remote(to, bar, make_float2(m.A[0], m.b[0]));
+    }
+  }
+  __device__ __forceinline__ bool wait(int s, int* err) {
+    if (mbar_wait_bounded(&arrived[s & 1], (s >> 1) & 1)) return true;
+    raise_error(err, DL_DEVERR_WAIT_TIMEOUT);
+    return false;
+  }
+};
+
+// Grid (channel tiles * N, rows), clusters of N along x; PC channels a lane; a
+// ring of S stages.
+template <typename TX, int MODE, int PC, bool CLUSTER, int S>
+__global__ void __launch_bounds__(kScanThreads) scan_kernel(ScanArgs a, int N) {
+  using Stage = ScanStage<TX, MODE, PC>;
+  extern __shared__ __align__(16) unsigned char ring_bytes[];
+  Stage* const ring = reinterpret_cast<Stage*>(ring_bytes);
+  __shared__ ScanMap<PC> part[kScanWarps][32];  // each warp's tokens
+  __shared__ ScanExchange<PC> ex;
 
   const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int rank = CLUSTER ? static_cast<int>(cluster_rank()) : 0;
-  const int c = (static_cast<int>(blockIdx.x) / N) * (32 * V) + lane * V;
+  const int c0 = (static_cast<int>(blockIdx.x) / N) * 32 * PC, c = c0 + (MODE == WIDE ? PC * lane : lane);
   const int r = blockIdx.y;
   const bool tell = blockIdx.x == 0 && threadIdx.x == 0;
   long long t0, n;
   const int slot = row_slot(a.slot_idx, a.slots, r, a.err, tell);
   if (slot < 0) return;  // the same for every CTA of the cluster
   if (!scan_row(a, r, tell, &t0, &n)) return;
-  const bool live = c < a.C;  // C % V == 0
-
-  float carry[V];  // state before the cluster's current N chunks
+  bool live[PC];
 #pragma unroll
-  for (int j = 0; j < V; ++j)
-    carry[j] = live && a.h0 ? a.h0[static_cast<long long>(slot) * a.C + c + j] : 0.f;
+  for (int j = 0; j < PC; ++j) live[j] = c + ch_step<MODE>(j) < a.C;
+  const long long pool = static_cast<long long>(slot) * a.C + c;
+  float carry[PC];  // state before the cluster's current N chunks
+  load_row<MODE>(carry, a.h0 ? a.h0 + pool : nullptr, live);
 
-  ScanTile<TX, V> tile;
-  const long long first = static_cast<long long>(rank) * kScanChunk + w * kScanTok;
-  const long long stride = static_cast<long long>(N) * kScanChunk;
-  const int steps = static_cast<int>((n + stride - 1) / stride);
-  if (steps > 0) tile.load(a, t0, first, n, c, live);
-  if constexpr (CLUSTER) cluster_sync();  // every CTA of the cluster runs before its shared memory is written
+  const TX* const px = static_cast<const TX*>(a.x);
   TX* const out = static_cast<TX*>(a.h);
+  const long long stride = static_cast<long long>(N) * kScanChunk, mine = static_cast<long long>(rank) * kScanChunk;
+  const int steps = static_cast<int>((n + stride - 1) / stride);
+  auto issue = [&](int s) {
+    if (s < steps) {
+      ring[s % S].d.load(a.log_decay, t0, s * stride + mine, n, c0, a.C, a.total);
+      ring[s % S].x.load(px, t0, s * stride + mine, n, c0, a.C, a.total);
+    }
+    copy_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < S - 1 + (S == 1); ++s) issue(s);
+  if constexpr (CLUSTER) ex.start();
 
   for (int s = 0; s < steps; ++s) {
-    const long long t = s * stride + first;
-    const int buf = s & 1;
-    float al[kScanTok][V];
-    Pack<TX, V> xs[kScanTok];
-    float A[V], b[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      A[j] = 1.f;
-      b[j] = 0.f;
-    }
+    const long long t = s * stride + mine + w * kScanTok;
+    copy_wait<S == 1 ? 0 : S - 2>();
+    __syncthreads();  // stage s is here for all warps, and all have left the stage before it and `part`
+    if constexpr (S > 1) issue(s + S - 1);
+
+    const Stage& st = ring[s % S];
+    const unsigned first = static_cast<unsigned>((t0 + s * stride + mine) * a.C + c0);
+    float al[kScanTok][PC];
+    Pack<TX, PC> x[kScanTok];
+    ScanMap<PC> own;
+    own.identity();
 #pragma unroll
     for (int i = 0; i < kScanTok; ++i) {
-      xs[i] = tile.x[i];
+      const Pack<float, PC> d = st.d.get(w * kScanTok + i, lane, first, a.C);
+      x[i] = st.x.get(w * kScanTok + i, lane, first, a.C);
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        al[i][j] = expf(tile.d[i].v[j]);
-        b[j] = fmaf(al[i][j], b[j], to_f32(xs[i].v[j]));
-        A[j] *= al[i][j];
+      for (int j = 0; j < PC; ++j) {
+        al[i][j] = decay_of(d.v[j]);
+        own.b[j] = fmaf(al[i][j], own.b[j], to_f32(x[i].v[j]));
+        own.A[j] *= al[i][j];
       }
     }
-    if (s + 1 < steps) tile.load(a, t0, t + stride, n, c, live);
-#pragma unroll
-    for (int j = 0; j < V; ++j) part[buf][w][lane * V + j] = make_float2(A[j], b[j]);
+    part[w][lane] = own;
     __syncthreads();
+    if constexpr (S == 1) issue(s + 1);
 
-    // (pA, pb): the chunk's warps before this one; the last warp adds its own
-    // and hands the chunk's total to every CTA of the cluster
-    float pA[V], pb[V];
+    ScanMap<PC> before;  // the chunk's warps before this one
+    before.identity();
+    for (int i = 0; i < w; ++i) before.then(part[i][lane]);
+    float h[PC];  // state before this chunk
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      pA[j] = 1.f;
-      pb[j] = 0.f;
-    }
-    for (int i = 0; i < w; ++i)
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float2 q = part[buf][i][lane * V + j];
-        pb[j] = fmaf(q.x, pb[j], q.y);
-        pA[j] *= q.x;
-      }
-    float base[V];  // state before this chunk
+    for (int j = 0; j < PC; ++j) h[j] = carry[j];
     if constexpr (CLUSTER) {
       if (w == kScanWarps - 1) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float tb = fmaf(A[j], pb[j], b[j]), tA = pA[j] * A[j];
-          for (int q = 0; q < N; ++q) store_remote(remote_smem(&tot[buf][rank][lane * V + j], q), tA, tb);
-        }
+        ScanMap<PC> all = before;
+        all.then(own);
+        ex.send(s, N, rank, all);
       }
-      cluster_sync();
+      if (!ex.wait(s, a.err)) break;
+      for (int q = 0; q < N; ++q) {
+        if (q == rank) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) base[j] = carry[j];
-      for (int q = 0; q < N; ++q)
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          if (q == rank) base[j] = carry[j];
-          const float2 m = tot[buf][q][lane * V + j];
-          carry[j] = fmaf(m.x, carry[j], m.y);
+          for (int j = 0; j < PC; ++j) h[j] = carry[j];
         }
+        ex.tot[s & 1][q][lane].apply(carry);
+      }
     } else {
-#pragma unroll
-      for (int j = 0; j < V; ++j) base[j] = carry[j];
-      float eA[V], eb[V];
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        eA[j] = pA[j];
-        eb[j] = pb[j];
-      }
-      for (int i = w; i < kScanWarps; ++i)
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float2 q = part[buf][i][lane * V + j];
-          eb[j] = fmaf(q.x, eb[j], q.y);
-          eA[j] *= q.x;
-        }
-#pragma unroll
-      for (int j = 0; j < V; ++j) carry[j] = fmaf(eA[j], carry[j], eb[j]);
+      ScanMap<PC> all = before;
+      for (int i = w; i < kScanWarps; ++i) all.then(part[i][lane]);
+      all.apply(carry);
     }
-
-    if (a.ckpt && w == 0 && live && t < n) {
-      const long long row = t0 / kScanChunk + r + t / kScanChunk;
-#pragma unroll
-      for (int j = 0; j < V; ++j) a.ckpt[row * a.C + c + j] = base[j];
-    }
-    float hv[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) hv[j] = fmaf(pA[j], base[j], pb[j]);
+    if (a.ckpt && w == 0 && t < n)
+      store_row<MODE>(a.ckpt + (t0 / kScanChunk + r + t / kScanChunk) * a.C + c, h, live);
+    before.apply(h);
     TX* po = out + (t0 + t) * a.C + c;
+    const int left = static_cast<int>(n - t < kScanTok ? n - t : kScanTok);
 #pragma unroll
     for (int i = 0; i < kScanTok; ++i) {
-      Pack<TX, V> o;
+      Pack<TX, PC> o;
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        hv[j] = fmaf(al[i][j], hv[j], to_f32(xs[i].v[j]));
-        o.v[j] = from_f32<TX>(hv[j]);
+      for (int j = 0; j < PC; ++j) {
+        h[j] = fmaf(al[i][j], h[j], to_f32(x[i].v[j]));
+        o.v[j] = from_f32<TX>(h[j]);
       }
-      if (live && t + i < n) store_stream<TX, V>(po + static_cast<long long>(i) * a.C, o);
+      if (i < left) store_out<MODE>(po, o, live);
+      po += a.C;
     }
   }
-  if (a.h_last && live && rank == 0 && w == 0) {
-#pragma unroll
-    for (int j = 0; j < V; ++j) a.h_last[static_cast<long long>(slot) * a.C + c + j] = carry[j];
-  }
+  copy_wait<0>();
+  if (a.h_last && rank == 0 && w == 0) store_row<MODE>(a.h_last + pool, carry, live);
 }
 
 // Backward.  With G_t the gradient of h_t,
@@ -239,170 +383,142 @@ __global__ void __launch_bounds__(kScanWarps * 32) scan_kernel(ScanArgs a, int N
 // rounded to its type, which would cost dlog_decay its precision; so h_{t-1}
 // is formed again in fp32 from the state before the chunk, which the forward
 // pass left in `ckpt` (4 bytes for every 64 tokens and channel).
-template <typename TX, int V, bool CLUSTER>
-__global__ void __launch_bounds__(kScanWarps * 32) scan_backward_kernel(ScanArgs a, int N) {
-  __shared__ float2 part[2][kScanWarps][32 * V];  // each warp's (A, b) forwards
-  __shared__ float back[2][kScanWarps][32 * V];   // and its b backwards
-  __shared__ float2 tot[2][CLUSTER ? 16 : 1][32 * V];
+template <typename TX, int MODE, int PC, bool CLUSTER, int S>
+__global__ void __launch_bounds__(kScanThreads) scan_backward_kernel(ScanArgs a, int N) {
+  using Stage = ScanBackStage<TX, MODE, PC>;
+  extern __shared__ __align__(16) unsigned char ring_bytes[];
+  Stage* const ring = reinterpret_cast<Stage*>(ring_bytes);
+  __shared__ ScanMap<PC> part[kScanWarps][32], back[kScanWarps][32];  // each warp's tokens, forwards and backwards
+  __shared__ ScanExchange<PC> ex;
 
   const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int rank = CLUSTER ? static_cast<int>(cluster_rank()) : 0;
-  const int c = (static_cast<int>(blockIdx.x) / N) * (32 * V) + lane * V;
+  const int c0 = (static_cast<int>(blockIdx.x) / N) * 32 * PC, c = c0 + (MODE == WIDE ? PC * lane : lane);
   const int r = blockIdx.y;
   long long t0, n;
   if (!scan_row(a, r, blockIdx.x == 0 && threadIdx.x == 0, &t0, &n)) return;
-  const bool live = c < a.C;
-
-  float carry[V];  // R behind the cluster's current N chunks
+  bool live[PC];
 #pragma unroll
-  for (int j = 0; j < V; ++j)
-    carry[j] = live && a.dh_last ? a.dh_last[static_cast<long long>(r) * a.C + c + j] : 0.f;
+  for (int j = 0; j < PC; ++j) live[j] = c + ch_step<MODE>(j) < a.C;
+  const long long row_at = static_cast<long long>(r) * a.C + c;
+  float carry[PC];  // R behind the cluster's current N chunks
+  load_row<MODE>(carry, a.dh_last ? a.dh_last + row_at : nullptr, live);
 
-  const long long first = static_cast<long long>(rank) * kScanChunk + w * kScanTok;
-  const long long stride = static_cast<long long>(N) * kScanChunk;
-  const int steps = static_cast<int>((n + stride - 1) / stride);
-  const TX* const dh = static_cast<const TX*>(a.dh);
+  const TX* const px = static_cast<const TX*>(a.x);
+  const TX* const pg = static_cast<const TX*>(a.dh);
   TX* const dx = static_cast<TX*>(a.dx);
-  if constexpr (CLUSTER) cluster_sync();
+  const long long stride = static_cast<long long>(N) * kScanChunk, mine = static_cast<long long>(rank) * kScanChunk;
+  const int steps = static_cast<int>((n + stride - 1) / stride);
+  auto issue = [&](int k) {  // k-th from the end
+    if (k < steps) {
+      const long long t = (steps - 1 - k) * stride + mine;
+      ring[k % S].d.load(a.log_decay, t0, t, n, c0, a.C, a.total);
+      ring[k % S].x.load(px, t0, t, n, c0, a.C, a.total);
+      ring[k % S].g.load(pg, t0, t, n, c0, a.C, a.total);
+    }
+    copy_commit();
+  };
+#pragma unroll
+  for (int k = 0; k < S - 1 + (S == 1); ++k) issue(k);
+  if constexpr (CLUSTER) ex.start();
 
-  for (int s = steps - 1; s >= 0; --s) {
-    const long long t = s * stride + first;
-    const int buf = s & 1;
-    ScanTile<TX, V> tile;
-    Pack<TX, V> g[kScanTok];
-    tile.load(a, t0, t, n, c, live);
-    const long long at = (t0 + t) * a.C + c;
+  for (int k = 0; k < steps; ++k) {
+    const long long chunk = (steps - 1 - k) * static_cast<long long>(N) + rank, t = chunk * kScanChunk + w * kScanTok;
+    float h[PC];  // state before this chunk
+    load_row<MODE>(h, chunk * kScanChunk < n ? a.ckpt + (t0 / kScanChunk + r + chunk) * a.C + c : nullptr, live);
+    copy_wait<S == 1 ? 0 : S - 2>();
+    __syncthreads();
+    if constexpr (S > 1) issue(k + S - 1);
+
+    const Stage& st = ring[k % S];
+    const unsigned first = static_cast<unsigned>((t0 + chunk * kScanChunk) * a.C + c0);
+    float al[kScanTok][PC];
+    Pack<TX, PC> x[kScanTok], g[kScanTok];
+    ScanMap<PC> own, own_back;
+    own.identity();
+    own_back.identity();
 #pragma unroll
     for (int i = 0; i < kScanTok; ++i) {
-      if (live && t + i < n) {
-        g[i] = load_stream<TX, V>(dh + at + static_cast<long long>(i) * a.C);
-      } else {
+      const Pack<float, PC> d = st.d.get(w * kScanTok + i, lane, first, a.C);
+      x[i] = st.x.get(w * kScanTok + i, lane, first, a.C);
+      g[i] = st.g.get(w * kScanTok + i, lane, first, a.C);
 #pragma unroll
-        for (int j = 0; j < V; ++j) g[i].v[j] = from_f32<TX>(0.f);
+      for (int j = 0; j < PC; ++j) {
+        al[i][j] = decay_of(d.v[j]);
+        own.b[j] = fmaf(al[i][j], own.b[j], to_f32(x[i].v[j]));
+        own.A[j] *= al[i][j];
       }
     }
-    float base[V];  // state before this chunk
-    {
-      const long long chunk = t / kScanChunk;
 #pragma unroll
-      for (int j = 0; j < V; ++j)
-        base[j] = live && chunk * kScanChunk < n ? a.ckpt[(t0 / kScanChunk + r + chunk) * a.C + c + j] : 0.f;
-    }
-    float al[kScanTok][V], A[V], b[V], e[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      A[j] = 1.f;
-      b[j] = 0.f;
-      e[j] = 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < kScanTok; ++i)
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        al[i][j] = expf(tile.d[i].v[j]);
-        b[j] = fmaf(al[i][j], b[j], to_f32(tile.x[i].v[j]));
-        A[j] *= al[i][j];
-      }
+    for (int j = 0; j < PC; ++j) own_back.A[j] = own.A[j];
 #pragma unroll
     for (int i = kScanTok - 1; i >= 0; --i)
 #pragma unroll
-      for (int j = 0; j < V; ++j) e[j] = al[i][j] * (to_f32(g[i].v[j]) + e[j]);
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      part[buf][w][lane * V + j] = make_float2(A[j], b[j]);
-      back[buf][w][lane * V + j] = e[j];
-    }
+      for (int j = 0; j < PC; ++j) own_back.b[j] = al[i][j] * (to_f32(g[i].v[j]) + own_back.b[j]);
+    part[w][lane] = own;
+    back[w][lane] = own_back;
     __syncthreads();
+    if constexpr (S == 1) issue(k + 1);
 
-    // state before this warp's tokens
-    for (int i = 0; i < w; ++i)
+    for (int i = 0; i < w; ++i) part[i][lane].apply(h);  // state before this warp's tokens
+    ScanMap<PC> behind;                                  // the chunk's warps behind this one
+    behind.identity();
+    for (int i = kScanWarps - 1; i > w; --i) behind.then(back[i][lane]);
+    float R[PC];
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float2 q = part[buf][i][lane * V + j];
-        base[j] = fmaf(q.x, base[j], q.y);
-      }
-    // (pA, pe): the chunk's warps behind this one
-    float pA[V], pe[V], R[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      pA[j] = 1.f;
-      pe[j] = 0.f;
-    }
-    for (int i = kScanWarps - 1; i > w; --i)
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float q = part[buf][i][lane * V + j].x;
-        pe[j] = fmaf(q, pe[j], back[buf][i][lane * V + j]);
-        pA[j] *= q;
-      }
+    for (int j = 0; j < PC; ++j) R[j] = carry[j];
     if constexpr (CLUSTER) {
       if (w == 0) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float te = fmaf(A[j], pe[j], e[j]), tA = pA[j] * A[j];
-          for (int q = 0; q < N; ++q) store_remote(remote_smem(&tot[buf][rank][lane * V + j], q), tA, te);
-        }
+        ScanMap<PC> all = behind;
+        all.then(own_back);
+        ex.send(k, N, rank, all);
       }
-      cluster_sync();
+      if (!ex.wait(k, a.err)) break;
+      for (int q = N - 1; q >= 0; --q) {
+        if (q == rank) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) R[j] = carry[j];
-      for (int q = N - 1; q >= 0; --q)
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          if (q == rank) R[j] = carry[j];
-          const float2 m = tot[buf][q][lane * V + j];
-          carry[j] = fmaf(m.x, carry[j], m.y);
+          for (int j = 0; j < PC; ++j) R[j] = carry[j];
         }
+        ex.tot[k & 1][q][lane].apply(carry);
+      }
     } else {
-      float eA[V], ee[V];
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        R[j] = carry[j];
-        eA[j] = pA[j];
-        ee[j] = pe[j];
-      }
-      for (int i = w; i >= 0; --i)
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float q = part[buf][i][lane * V + j].x;
-          ee[j] = fmaf(q, ee[j], back[buf][i][lane * V + j]);
-          eA[j] *= q;
-        }
-#pragma unroll
-      for (int j = 0; j < V; ++j) carry[j] = fmaf(eA[j], carry[j], ee[j]);
+      ScanMap<PC> all = behind;
+      for (int i = w; i >= 0; --i) all.then(back[i][lane]);
+      all.apply(carry);
     }
-
-    float hp[kScanTok][V];  // a_t h_{t-1}
-#pragma unroll
-    for (int j = 0; j < V; ++j) R[j] = fmaf(pA[j], R[j], pe[j]);
+    behind.apply(R);
+    float hp[kScanTok][PC];  // a_t h_{t-1}
 #pragma unroll
     for (int i = 0; i < kScanTok; ++i)
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        hp[i][j] = al[i][j] * base[j];
-        base[j] = hp[i][j] + to_f32(tile.x[i].v[j]);
+      for (int j = 0; j < PC; ++j) {
+        hp[i][j] = al[i][j] * h[j];
+        h[j] = hp[i][j] + to_f32(x[i].v[j]);
       }
+    const int left = static_cast<int>(n - t < kScanTok ? n - t : kScanTok);
+    TX* ox = dx + (t0 + t + kScanTok - 1) * a.C + c;
+    float* od = a.dlog_decay + (t0 + t + kScanTok - 1) * a.C + c;
 #pragma unroll
     for (int i = kScanTok - 1; i >= 0; --i) {
-      Pack<TX, V> ox;
-      Pack<float, V> od;
+      Pack<TX, PC> vx;
+      Pack<float, PC> vd;
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
+      for (int j = 0; j < PC; ++j) {
         const float G = to_f32(g[i].v[j]) + R[j];
-        ox.v[j] = from_f32<TX>(G);
-        od.v[j] = hp[i][j] * G;
+        vx.v[j] = from_f32<TX>(G);
+        vd.v[j] = hp[i][j] * G;
         R[j] = al[i][j] * G;
       }
-      if (live && t + i < n) {
-        store_stream<TX, V>(dx + at + static_cast<long long>(i) * a.C, ox);
-        store_stream<float, V>(a.dlog_decay + at + static_cast<long long>(i) * a.C, od);
+      if (i < left) {
+        store_out<MODE>(ox, vx, live);
+        store_out<MODE>(od, vd, live);
       }
+      ox -= a.C;
+      od -= a.C;
     }
   }
-  if (a.dh0 && live && rank == 0 && w == 0) {
-#pragma unroll
-    for (int j = 0; j < V; ++j) a.dh0[static_cast<long long>(r) * a.C + c + j] = carry[j];
-  }
+  copy_wait<0>();
+  if (a.dh0 && rank == 0 && w == 0) store_row<MODE>(a.dh0 + row_at, carry, live);
 }
 
 // One token for every row: h = exp(log_decay) state + x, rounded to the

@@ -1,10 +1,12 @@
 """The gated linear recurrence (forward, backward, single token) against its definition in 64 bits.
 
-Bounds.  A decay a = exp(d) is off by at most 2 units in the last place (expf; 4 U, U = 2^-24), each product of
-decays adds one rounding (U) a token, each multiply-add one (U); folding runs of tokens adds at most one product and
-one multiply-add a token again.  So every token perturbs the state by at most 8 U of its magnitude sum
-H_t = a_t H_{t-1} + |x_t|, and the error obeys E_t = a_t E_{t-1} + 8 U H_t.  The backward pass obeys the same with
-|dh| in place of |x|.  Outputs in bf16 add half a step of their own.
+Bounds.  U = 2^-24, half an ulp of fp32, relative.  A decay a = 2^fl(d log2 e) is off by 2^-22 = 4 U of itself (ex2)
+and by 1.5 |d| U of itself: log2 e and the product are rounded, 0.5 + 1 U of an exponent of |d| log2 e, and the
+derivative of 2^t is ln 2 of it.  Each product of decays adds one rounding (U) a token, each multiply-add one (U);
+folding runs of tokens adds at most one product and one multiply-add a token again.  So token t perturbs the state by
+at most (8 + 1.5 |d_t|) U of its magnitude sum H_t = a_t H_{t-1} + |x_t| (a decay's own error meets a_t H_{t-1} only),
+and the error obeys E_t = a_t E_{t-1} + (8 + 1.5 |d_t|) U a_t H_{t-1} + 8 U |x_t|.  The backward pass obeys the same
+with |dh| in place of |x|.  Outputs in bf16 add half a step of their own.
 """
 import pytest
 import torch
@@ -29,6 +31,7 @@ def _inputs(lens, C, dtype, seed, strong=False):
 def _reference(lens, x, d, h0, dh=None, dlast=None):
     """h, its bound, h_last, its bound; with dh also dx, dlog_decay, dh0 and theirs."""
     x, a, h0 = x.double(), d.double().exp(), h0.double()
+    c = (8 + 1.5 * d.double().abs().clamp(max=200.0)) * U      # past 200 a decay is 0 either way
     C = x.shape[1]
     h, eh = torch.zeros_like(x), torch.zeros_like(x)
     hp, ehp = torch.zeros_like(x), torch.zeros_like(x)      # a_t h_{t-1}
@@ -39,9 +42,9 @@ def _reference(lens, x, d, h0, dh=None, dlast=None):
     for r, n in enumerate(lens):
         s, m, e = h0[r], h0[r].abs(), torch.zeros(C).double()
         for t in range(t0, t0 + n):
-            hp[t], ehp[t] = a[t] * s, a[t] * (e + C_ERR * m)
-            s, m = a[t] * s + x[t], a[t] * m + x[t].abs()
-            e = a[t] * e + C_ERR * m
+            hp[t], ehp[t] = a[t] * s, a[t] * (e + c[t] * m)
+            e = ehp[t] + C_ERR * x[t].abs()
+            s, m = hp[t] + x[t], a[t] * m + x[t].abs()
             h[t], eh[t] = s, e
         last[r], elast[r] = s, e
         if dh is not None:
@@ -51,7 +54,7 @@ def _reference(lens, x, d, h0, dh=None, dlast=None):
                 G, m = dh[t].double() + R, dh[t].double().abs() + m
                 e = e + C_ERR * m
                 dx[t], edx[t] = G, e
-                R, m, e = a[t] * G, a[t] * m, a[t] * (e + C_ERR * m)
+                R, m, e = a[t] * G, a[t] * m, a[t] * (e + c[t] * m)
             dh0[r], edh0[r] = R, e
         t0 += n
     if dh is None:
@@ -210,22 +213,30 @@ def test_invalid_ranges_are_skipped_and_reported():
         assert (out[4:] == -1.0).all()
 
 
-def test_unaligned_views_and_in_place():
-    """Rows that start on odd addresses take the narrow loads; h may overwrite x."""
-    from recurrent_state_update_deltalog_b200 import gated_scan_prefill
-    n, C = 100, 64
-    x, d, h0, _, _ = _inputs([n], C, torch.bfloat16, 5)
-    flat, fd = torch.zeros(n * C + 1, dtype=torch.bfloat16, device="cuda"), torch.zeros(n * C + 1, device="cuda")
-    xv, dv = flat[1:].view(n, C), fd[1:].view(n, C)
-    xv.copy_(x)
-    dv.copy_(d)
-    ref = _reference([n], x, d, h0)
-    a, b = h0.cuda(), h0.cuda()
-    want = gated_scan_prefill(x.cuda(), d.cuda(), a, _cu([n]))
-    got = gated_scan_prefill(xv, dv, b, _cu([n]), out=xv)
-    assert got.data_ptr() == xv.data_ptr()
-    assert_within(got, ref[0], rounded(ref[1], ref[0], torch.bfloat16), "h")
-    assert torch.equal(got, want) and torch.equal(a, b)
+@pytest.mark.parametrize("n,C", [(100, 64), (700, 33), (5, 72)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_unaligned_views_and_in_place(n, C, dtype):
+    """Tensors that start on odd addresses take element-wise loads; h may overwrite x."""
+    from recurrent_state_update_deltalog_b200 import gated_scan, gated_scan_prefill
+    x, d, h0, dh, dlast = _inputs([n], C, dtype, 5)
+    ref = _reference([n], x, d, h0, dh, dlast)
+
+    def odd(t):
+        flat = torch.zeros(t.numel() + 1, dtype=t.dtype, device="cuda")
+        return flat[1:].view(t.shape).copy_(t)
+
+    xv, dv = odd(x).requires_grad_(), odd(d).requires_grad_()
+    h, last = gated_scan(xv, dv, h0.cuda(), cu_seqlens=_cu([n]))
+    dx, dld = torch.autograd.grad((h, last), (xv, dv), (odd(dh), dlast.cuda()))
+    assert_within(h, ref[0], rounded(ref[1], ref[0], dtype), "h")
+    assert_within(dx, ref[4], rounded(ref[5], ref[4], dtype), "dx")
+    assert_within(dld, ref[6], rounded(ref[7], ref[6], torch.float32), "dlog_decay")
+    for xs, ds in ((odd(x), odd(d)), (x.cuda(), d.cuda())):
+        state = h0.cuda()
+        got = gated_scan_prefill(xs, ds, state, _cu([n]), out=xs)
+        assert got.data_ptr() == xs.data_ptr()
+        assert_within(got, ref[0], rounded(ref[1], ref[0], dtype), "h")
+        assert_within(state, ref[2], rounded(ref[3], ref[2], torch.float32), "state")
 
 
 def test_stream_and_captured_graphs():
