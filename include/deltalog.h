@@ -500,12 +500,17 @@ int dl_block_norm_backward(int rows, int D, int groups, int in_dtype, const void
  * Hq a multiple of Hkv; d in {64, 128}; page_size a power of two; pointers of
  * typed tensors 16-byte aligned.  The split over the length follows max_pages
  * (or the window), so a table no wider than needed is fastest.  Scores and
- * sums are fp32; with bf16 the weights enter their product with v as bf16. */
+ * sums are fp32; with bf16 the weights enter their product with v as bf16.
+ *   workspace   16-byte aligned buffer of dl_paged_attention_workspace bytes
+ *               (0 where tables are short), not to be used by two calls that
+ *               may overlap; NULL: a coarser split, slower on long tables. */
+int dl_paged_attention_workspace(int rows, int Hq, int Hkv, int d, int in_dtype, int page_size,
+                                 int max_pages, int window, size_t* bytes);
 int dl_paged_attention(const int* slot_idx, int slots, int rows, int Hq, int Hkv, int d, int in_dtype,
                        int page_size, long long num_pages, int max_pages, const int* table,
                        const int* lens, int window, float scale, const void* q, const void* k,
-                       const void* v, void* k_pages, void* v_pages, void* out, int* dev_err,
-                       void* stream);
+                       const void* v, void* k_pages, void* v_pages, void* out, void* workspace,
+                       int* dev_err, void* stream);
 
 /* Copy prompts into the pages: tokens [cu_seqlens[r], cu_seqlens[r + 1]) of k
  * and v (typed [total][Hkv][d]) to positions starts[s] + 0, 1, ... of row r's

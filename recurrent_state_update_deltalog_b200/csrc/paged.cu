@@ -1,5 +1,6 @@
 // Entry points of the paged-cache attention (kernels in paged.cuh).
 #include "paged.cuh"
+#include "launch.cuh"
 
 #include <limits.h>
 #include <math.h>
@@ -22,7 +23,7 @@ int check(const int* slot_idx, int slots, int rows, int Hkv, int d, int dtype, i
   if (page_size < 1 || page_size > (1 << 20) || (page_size & (page_size - 1)))
     return unsupported("page_size not a power of two in [1, 2^20]");
   if (num_pages > INT_MAX || Hkv > 65535) return unsupported("page ids are 32-bit, at most 65535 key-value heads");
-  if (static_cast<long long>(max_pages) * page_size > INT_MAX - 65536) return unsupported("positions are 32-bit");
+  if (static_cast<long long>(max_pages) * page_size > (1 << 30)) return unsupported("more than 2^30 positions a slot");
   if (rows == 0) return DL_OK;
   if (slot_idx ? slots < 1 : slots < rows) return bad("fewer slots than rows");
   if (!table && max_pages > 0) return bad("null table");
@@ -42,31 +43,77 @@ int shift_of(int page_size) {
   return s;
 }
 
-// Launches one kernel with N CTAs a cluster.
-cudaError_t launch(void (*kern)(PagedArgs, int), const PagedArgs& a, int rows, int warps, size_t smem, int N, cudaStream_t st) {
-  if (smem + 1024 > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
+constexpr int kSms = 148;
+
+// How the tokens are shared out.
+struct Split {
+  int heads;        // query heads of a CTA
+  int head_blocks;  // CTAs' head groups a key-value head
+  bool even;        // equal runs of all tiles, through a workspace and a second launch
+  int ctas;         // of the whole launch (even), else of a cluster
+};
+
+// Clusters of up to 8 CTAs, until the launch has three CTAs for every two SMs,
+// as long as every warp finds two tiles in the longest row the table allows.
+// The even form if a warp would then have more than eight.  B200, bf16, d = 128,
+// 8 key-value heads of 4, clusters / even: 8 rows of 1024 tokens (4 tiles a
+// warp) 13.5 / 16.8 us; 32 ragged rows of up to 4096 tokens (64) 65 / 47 us.
+Split split_of(int rows, int G, int Hkv, int dtype, long long longest) {
+  Split s{};
+  s.heads = dtype == DL_BF16 ? (G > 8 ? 16 : 8) : G > 2 ? 4 : G;
+  s.head_blocks = (G + s.heads - 1) / s.heads;
+  const long long units = static_cast<long long>(rows) * Hkv * s.head_blocks;
+  const long long tiles = (longest + dl::kTile - 1) / dl::kTile;
+  s.ctas = 1;
+  while (s.ctas < 8 && 2 * units * s.ctas < 3 * kSms && 2 * s.ctas * 4 * 2 <= tiles) s.ctas *= 2;
+  if (tiles > 8 * 4 * s.ctas && rows <= dl::kPagedRows) {
+    s.even = true;
+    const long long runs = (units * tiles + dl::kPagedRun - 1) / dl::kPagedRun;  // most that have work
+    const int resident = kSms * (s.heads > 8 ? 2 : 3);
+    s.ctas = static_cast<int>(runs < resident ? runs : resident);
   }
-  return dl::launch_cluster(kern, dim3(static_cast<unsigned>(a.Hkv) * a.head_blocks * N, rows), warps * 32, smem, st, N, a, N);
+  return s;
 }
 
-template <int D, int NT, int W, int TT>
-cudaError_t bf16(const PagedArgs& a, int rows, int N, cudaStream_t st) {
-  return launch(dl::paged_bf16_kernel<D, NT, W, TT>, a, rows, W, sizeof(float) * W * 8 * NT * (D + 2), N, st);
+size_t plan_bytes(int rows) { return (sizeof(long long) * (rows + 2) + 15) / 16 * 16; }
+size_t workspace_bytes(const Split& s, int rows, int d) {
+  return s.even ? plan_bytes(rows) + sizeof(float) * 2 * s.ctas * s.heads * (d + 2) : 0;
 }
 
-template <int D, int HT, int W>
-cudaError_t f32(const PagedArgs& a, int rows, int N, cudaStream_t st) {
-  return launch(dl::paged_f32_kernel<D, HT, W>, a, rows, W, sizeof(float) * HT * (W * 4 * (D + 2) + D), N, st);
+long long longest_row(int max_pages, int page_size, int window) {
+  const long long n = static_cast<long long>(max_pages) * page_size;
+  return window > 0 && window < n ? window : n;
 }
 
-// CTAs a (row, head group): enough for about three CTAs an SM, no more than
-// the longest possible row has work for (`most` warps' shares).
-int cluster_of(long long units, int warps, long long most) {
-  int n = 1;
-  while (n < 8 && units * n < 3 * 148 && 2ll * n * warps <= most) n *= 2;
-  return n;
+using Kernel = void (*)(PagedArgs, int);
+
+template <typename T, int D, int HT>
+cudaError_t launch(Kernel clusters, Kernel even, const PagedArgs& a, const Split& s, int warps, size_t smem, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(s.even ? even : clusters, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  if (!s.even)
+    return dl::launch_cluster(clusters, dim3(static_cast<unsigned>(a.Hkv) * s.head_blocks * s.ctas, a.rows), warps * 32, smem, st, s.ctas,
+                              a, s.ctas);
+  even<<<s.ctas, warps * 32, smem, st>>>(a, 1);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const dim3 heads(a.Hkv * a.G, a.rows);
+  // few units: each is cut into many pieces
+  return static_cast<long long>(a.rows) * a.Hkv * s.head_blocks < kSms
+             ? dl::launch_maybe_pdl(dl::paged_join_kernel<T, D, HT, 4>, heads, 4 * D, 0, st, true, a)
+             : dl::launch_maybe_pdl(dl::paged_join_kernel<T, D, HT, 1>, heads, D, 0, st, true, a);
+}
+
+template <int D, int NT, int TT>
+cudaError_t bf16(const PagedArgs& a, const Split& s, cudaStream_t st) {
+  return launch<__nv_bfloat16, D, 8 * NT>(dl::paged_bf16_kernel<D, NT, 4, TT, false>, dl::paged_bf16_kernel<D, NT, 4, TT, true>, a, s, 4,
+                                          sizeof(float) * 4 * 8 * NT * (D + 2), st);
+}
+
+template <int D, int HT>
+cudaError_t f32(const PagedArgs& a, const Split& s, cudaStream_t st) {
+  return launch<float, D, HT>(dl::paged_f32_kernel<D, HT, 4, false>, dl::paged_f32_kernel<D, HT, 4, true>, a, s, 4,
+                              sizeof(float) * HT * (16 * (D + 2) + D), st);
 }
 
 }  // namespace
@@ -75,8 +122,8 @@ extern "C" {
 
 int dl_paged_attention(const int* slot_idx, int slots, int rows, int Hq, int Hkv, int d, int in_dtype, int page_size,
                        long long num_pages, int max_pages, const int* table, const int* lens, int window, float scale,
-                       const void* q, const void* k, const void* v, void* k_pages, void* v_pages, void* out, int* dev_err,
-                       void* stream) {
+                       const void* q, const void* k, const void* v, void* k_pages, void* v_pages, void* out, void* workspace,
+                       int* dev_err, void* stream) {
   const int rc = check(slot_idx, slots, rows, Hkv, d, in_dtype, page_size, num_pages, max_pages, table);
   if (rc != DL_OK) return rc;
   if (Hq < 1 || Hq % Hkv) return bad("Hq not a positive multiple of Hkv");
@@ -87,6 +134,12 @@ int dl_paged_attention(const int* slot_idx, int slots, int rows, int Hq, int Hkv
   if ((k == nullptr) != (v == nullptr)) return bad("k and v go together");
   if (!aligned16({q, k, v, k_pages, v_pages, out})) return bad("pointer not 16-byte aligned");
   if (!dl::is_aligned(lens, 4) || !dl::is_aligned(dev_err, 4)) return bad("int pointer not 4-byte aligned");
+  if (!dl::is_aligned(workspace, 16)) return bad("workspace not 16-byte aligned");
+  Split s = split_of(rows, Hq / Hkv, Hkv, in_dtype, longest_row(max_pages, page_size, window));
+  if (s.even && !workspace) {  // the widest form without one
+    s.even = false;
+    s.ctas = 8;
+  }
   PagedArgs a{};
   a.q = q;
   a.k_new = k;
@@ -106,26 +159,33 @@ int dl_paged_attention(const int* slot_idx, int slots, int rows, int Hq, int Hkv
   a.G = Hq / Hkv;
   a.window = window;
   a.scale = scale * 1.44269504088896340736f;  // exponents in base 2
-  long long longest = static_cast<long long>(max_pages) * page_size;
-  if (window > 0 && window < longest) longest = window;
+  a.head_blocks = s.head_blocks;
+  a.rows = rows;
+  if (s.even) {
+    a.plan = static_cast<long long*>(workspace);
+    a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan_bytes(rows));
+  }
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (in_dtype == DL_BF16) {
-    const int nt = a.G > 8 ? 2 : 1;
-    a.head_blocks = (a.G + 8 * nt - 1) / (8 * nt);
-    const int n = cluster_of(static_cast<long long>(rows) * Hkv * a.head_blocks, 4, longest / 32);
-    if (d == 128) e = nt == 1 ? bf16<128, 1, 4, 1>(a, rows, n, st) : bf16<128, 2, 4, 1>(a, rows, n, st);
-    else e = nt == 1 ? bf16<64, 1, 4, 2>(a, rows, n, st) : bf16<64, 2, 4, 2>(a, rows, n, st);
+    if (d == 128) e = s.heads == 8 ? bf16<128, 1, 1>(a, s, st) : bf16<128, 2, 1>(a, s, st);
+    else e = s.heads == 8 ? bf16<64, 1, 2>(a, s, st) : bf16<64, 2, 2>(a, s, st);
+  } else if (d == 128) {
+    e = s.heads == 4 ? f32<128, 4>(a, s, st) : s.heads == 2 ? f32<128, 2>(a, s, st) : f32<128, 1>(a, s, st);
   } else {
-    const int ht = a.G > 2 ? 4 : a.G;
-    a.head_blocks = (a.G + ht - 1) / ht;
-    const int n = cluster_of(static_cast<long long>(rows) * Hkv * a.head_blocks, 16, longest / 4);
-    if (d == 128)
-      e = ht == 4 ? f32<128, 4, 4>(a, rows, n, st) : ht == 2 ? f32<128, 2, 4>(a, rows, n, st) : f32<128, 1, 4>(a, rows, n, st);
-    else
-      e = ht == 4 ? f32<64, 4, 4>(a, rows, n, st) : ht == 2 ? f32<64, 2, 4>(a, rows, n, st) : f32<64, 1, 4>(a, rows, n, st);
+    e = s.heads == 4 ? f32<64, 4>(a, s, st) : s.heads == 2 ? f32<64, 2>(a, s, st) : f32<64, 1>(a, s, st);
   }
   return e == cudaSuccess ? DL_OK : dl::launch_failed(e, "paged attention launch");
+}
+
+int dl_paged_attention_workspace(int rows, int Hq, int Hkv, int d, int in_dtype, int page_size, int max_pages, int window,
+                                 size_t* bytes) {
+  if (!bytes) return bad("null output pointer");
+  if (rows < 0 || Hkv < 1 || Hq < 1 || Hq % Hkv || d < 1 || page_size < 1 || max_pages < 0 || window < 0 ||
+      (in_dtype != DL_F32 && in_dtype != DL_BF16))
+    return bad("bad size or dtype");
+  *bytes = rows ? workspace_bytes(split_of(rows, Hq / Hkv, Hkv, in_dtype, longest_row(max_pages, page_size, window)), rows, d) : 0;
+  return DL_OK;
 }
 
 int dl_paged_write(const int* slot_idx, int slots, int rows, const int* cu_seqlens, long long total, int Hkv, int d,

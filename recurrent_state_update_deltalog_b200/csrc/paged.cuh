@@ -11,8 +11,12 @@
 // Bound: memory; each key and value is read once for all query heads of its
 // group (4 G flops an element of 2 bytes).  The tokens of one (row, key-value
 // head) are dealt out in tiles of 16 to the warps of a cluster of CTAs, whose
-// triples meet in distributed shared memory: one launch, no workspace, no
-// atomics, results independent of timing.
+// triples meet in distributed shared memory: one launch, no workspace.  Where
+// that would leave a warp more than eight tiles, the work is shared evenly
+// instead: as many CTAs as fit the GPU at once take equal runs of the list of
+// all tiles (row by row, head by head), however ragged the rows; the triples of
+// the (row, head)s that a run cuts go through a workspace, and a second launch
+// joins them.  No atomics; results do not depend on timing.
 //
 // bf16: warp MMAs (m16n8k16) with the cache as the 16-row operand and 8 query
 // heads as the columns, S^T = K Q^T and O^T = V^T P^T.  The contraction over
@@ -44,6 +48,12 @@ struct PagedArgs {
   int slots, max_pages, page_shift;
   int Hkv, G;             // G = Hq / Hkv query heads a key-value head
   int head_blocks;        // CTAs' head groups a key-value head
+  // shared evenly: each CTA's triples of the (row, head) it found begun [2i] and
+  // of the one it left unfinished [2i + 1], [2 * CTAs][HT][d + 2]; and the plan,
+  // [rows + 1] tiles before each row and [1] tiles of a CTA
+  float* parts;
+  long long* plan;
+  int rows;
   int window;             // 0: none
   float scale;            // times log2(e)
   // prompts
@@ -113,6 +123,87 @@ __device__ __forceinline__ bool paged_row(const PagedArgs& a, int r, bool tell, 
   return true;
 }
 
+constexpr int kTile = 16;        // tokens of a tile
+constexpr int kPagedRows = 1024; // rows of a launch that shares its tiles evenly
+constexpr int kPagedRun = 32;    // fewest tiles of its CTAs: 8 a warp
+
+// A piece of one (row, key-value head, head group): tiles [from, to) of the row.
+struct PagedPiece {
+  int r, slot, kvh, hb, first, len, from, to;
+  bool begun, unfinished;  // tiles of the unit before `from`, behind `to`
+};
+
+// The even sharing: this CTA's run of the list of all tiles.
+struct PagedRun {
+  long long at, end;  // list positions still to do
+  int r;              // row of `at`
+  const long long* before;  // shared: tiles before each row, [rows + 1]
+
+  // Every thread of the CTA takes part.  CTA 0 leaves the plan for the join.
+  __device__ __forceinline__ void start(const PagedArgs& a, long long* cum, int threads) {
+    const int units = a.Hkv * a.head_blocks;
+    for (int i = threadIdx.x; i < a.rows; i += threads) {
+      int slot, first, len;
+      const bool there = paged_row(a, i, blockIdx.x == 0, &slot, &first, &len) && len > 0;
+      cum[i + 1] = there ? static_cast<long long>((len + kTile - 1) / kTile - first / kTile) * units : 0;
+    }
+    if (threadIdx.x == 0) cum[0] = 0;
+    __syncthreads();
+    if (threadIdx.x < 32) {  // sums up to each row, 32 rows at a time
+      long long total = 0;
+      for (int base = 0; base < a.rows; base += 32) {
+        const int i = base + threadIdx.x;
+        long long v = i < a.rows ? cum[i + 1] : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long u = __shfl_up_sync(~0u, v, o);
+          if (static_cast<int>(threadIdx.x) >= o) v += u;
+        }
+        if (i < a.rows) cum[i + 1] = total + v;
+        total += __shfl_sync(~0u, v, 31);
+      }
+    }
+    __syncthreads();
+    const long long all = cum[a.rows], even = (all + gridDim.x - 1) / gridDim.x, run = even > kPagedRun ? even : kPagedRun;
+    if (blockIdx.x == 0) {
+      for (int i = threadIdx.x; i <= a.rows; i += threads) a.plan[i] = cum[i];
+      if (threadIdx.x == 0) a.plan[a.rows + 1] = run;
+    }
+    before = cum;
+    at = blockIdx.x * run < all ? blockIdx.x * run : all;
+    end = at + run < all ? at + run : all;
+    int lo = 0, hi = a.rows;  // last row with before[r] <= at
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (cum[mid] <= at) lo = mid;
+      else hi = mid;
+    }
+    r = lo;
+  }
+
+  __device__ __forceinline__ bool next(const PagedArgs& a, PagedPiece* p) {
+    if (at >= end) return false;
+    while (before[r + 1] <= at) ++r;  // rows without tiles
+    p->r = r;
+    paged_row(a, r, false, &p->slot, &p->first, &p->len);
+    const int units = a.Hkv * a.head_blocks, tile0 = p->first / kTile;
+    const int tiles = static_cast<int>((before[r + 1] - before[r]) / units);
+    const long long in = at - before[r];  // below 2^31 tiles a row and 65535 heads: often short
+    const int unit = in >> 32 ? static_cast<int>(in / tiles) : static_cast<int>(static_cast<unsigned>(in) / tiles);
+    const int from = static_cast<int>(in - static_cast<long long>(unit) * tiles);
+    const long long left = end - at;
+    const int n = left < tiles - from ? static_cast<int>(left) : tiles - from;
+    p->kvh = unit / a.head_blocks;
+    p->hb = unit % a.head_blocks;
+    p->from = tile0 + from;
+    p->to = p->from + n;
+    p->begun = from > 0;
+    p->unfinished = from + n < tiles;
+    at += n;
+    return true;
+  }
+};
+
 // Stores the new token's key and value of one (row, key-value head).
 template <typename T, int D>
 __device__ __forceinline__ void store_new(const PagedArgs& a, int r, int kvh, const int* table, int len) {
@@ -128,173 +219,321 @@ __device__ __forceinline__ void store_new(const PagedArgs& a, int r, int kvh, co
   reinterpret_cast<uint4*>(to)[u] = reinterpret_cast<const uint4*>(from)[u];
 }
 
-// Joins the NP triples of this CTA and then those of the cluster's N CTAs, and
-// writes the outputs of heads [h0, h0 + HT).  `o` [NP][HT][D], `ml` [NP][HT][2].
+// Joins the NP triples of this CTA, `o` [NP][HT][D] and `ml` [NP][HT][2], for a
+// piece of the heads [hb * HT, hb * HT + HT) of a key-value head.  A whole one
+// is written out, after the triples of the cluster's N CTAs have met; one that
+// a run cuts goes to a.parts.
 template <typename T, int D, int HT, int NP, int THREADS>
-__device__ __forceinline__ void join_and_store(const PagedArgs& a, float* o, float* ml, int r, int kvh, int h0, int N, int rank) {
-  __syncthreads();
+__device__ __forceinline__ void join_and_store(const PagedArgs& a, const PagedPiece& p, float* o, float* ml, int N, int rank) {
   __shared__ float top[HT][2];  // the CTA's (m, sum)
+  __syncthreads();
   for (int h = threadIdx.x; h < HT; h += THREADS) {
     float m = -INFINITY, l = 0.f;
-    for (int p = 0; p < NP; ++p) m = fmaxf(m, ml[(p * HT + h) * 2]);
-    for (int p = 0; p < NP; ++p) l += ml[(p * HT + h) * 2 + 1] * exp2_diff(ml[(p * HT + h) * 2], m);
+    for (int i = 0; i < NP; ++i) m = fmaxf(m, ml[(i * HT + h) * 2]);
+    for (int i = 0; i < NP; ++i) {
+      float* const q = ml + (i * HT + h) * 2;
+      q[0] = exp2_diff(q[0], m);  // weight of triple i from here on
+      l = fmaf(q[1], q[0], l);
+    }
     top[h][0] = m;
     top[h][1] = l;
   }
   __syncthreads();
+  float* const part =
+      p.begun || p.unfinished ? a.parts + (2ll * blockIdx.x + (p.begun ? 0 : 1)) * HT * (D + 2) : nullptr;
   for (int e = threadIdx.x; e < HT * D; e += THREADS) {
     const int h = e / D;
     float s = 0.f;
 #pragma unroll 4
-    for (int p = 0; p < NP; ++p) s += o[p * HT * D + e] * exp2_diff(ml[(p * HT + h) * 2], top[h][0]);
-    o[e] = s;  // element e of the first triple is read by this thread alone
+    for (int i = 0; i < NP; ++i) s = fmaf(o[i * HT * D + e], ml[(i * HT + h) * 2], s);
+    if (part) part[h * (D + 2) + e % D] = s;
+    else o[e] = s;  // element e of the first triple is read by this thread alone
+  }
+  if (part) {
+    if (threadIdx.x < 2 * HT) part[(threadIdx.x / 2) * (D + 2) + D + threadIdx.x % 2] = top[threadIdx.x / 2][threadIdx.x % 2];
+    return;
   }
   if (N > 1) cluster_sync();
   else __syncthreads();
   const int share = HT * D / N;  // N divides 8, HT * D is a multiple of 64
   for (int i = threadIdx.x; i < share; i += THREADS) {
     const int e = rank * share + i, h = e / D;
-    if (h0 + h >= a.G) continue;
+    if (p.hb * HT + h >= a.G) continue;
     float m = -INFINITY, l = 0.f, s = 0.f;
     for (int q = 0; q < N; ++q) m = fmaxf(m, N > 1 ? load_remote(remote_smem(&top[h][0], q)) : top[h][0]);
     for (int q = 0; q < N; ++q) {
       const float w = exp2_diff(N > 1 ? load_remote(remote_smem(&top[h][0], q)) : top[h][0], m);
-      l += w * (N > 1 ? load_remote(remote_smem(&top[h][1], q)) : top[h][1]);
-      s += w * (N > 1 ? load_remote(remote_smem(o + e, q)) : o[e]);
+      l = fmaf(w, N > 1 ? load_remote(remote_smem(&top[h][1], q)) : top[h][1], l);
+      s = fmaf(w, N > 1 ? load_remote(remote_smem(o + e, q)) : o[e], s);
     }
-    const long long head = static_cast<long long>(r) * a.Hkv * a.G + static_cast<long long>(kvh) * a.G + h0 + h;
+    const long long head = (static_cast<long long>(p.r) * a.Hkv + p.kvh) * a.G + p.hb * HT + h;
     static_cast<T*>(a.out)[head * D + e % D] = from_f32<T>(l == 0.f ? 0.f : s / l);
   }
   if (N > 1) cluster_sync();  // no CTA leaves while another reads its shared memory
 }
 
-// bf16.  Grid (Hkv * head_blocks * N, rows), clusters of N; W warps a CTA; NT
-// column tiles of 8 query heads; tiles of 16 tokens, TT at a time.
-template <int D, int NT, int W, int TT>
-__global__ void __launch_bounds__(W * 32) paged_bf16_kernel(PagedArgs a, int N) {
+// Joins what the runs have cut, and writes zeros for rows of length 0: grid
+// (Hq, rows), a CTA of GR groups of D threads, each over every GR-th triple.
+template <typename T, int D, int HT, int GR>
+__global__ void __launch_bounds__(GR * D) paged_join_kernel(PagedArgs a) {
+  __shared__ float sm[GR][D], sl[GR], sn[GR];
+  griddep_wait();
+  const int r = blockIdx.y, head = blockIdx.x, kvh = head / a.G, hb = head % a.G / HT, h = head % a.G % HT;
+  int slot, first, len;
+  if (!paged_row(a, r, false, &slot, &first, &len)) return;
+  const int grp = threadIdx.x / D, e = threadIdx.x % D;
+  T* const out = static_cast<T*>(a.out) + (static_cast<long long>(r) * a.Hkv * a.G + head) * D + e;
+  if (len == 0) {
+    if (grp == 0) *out = from_f32<T>(0.f);
+    return;
+  }
+  const int units = a.Hkv * a.head_blocks;
+  const long long begin = a.plan[r], tiles = (a.plan[r + 1] - begin) / units, run = a.plan[a.rows + 1];
+  const long long g0 = begin + (kvh * a.head_blocks + hb) * tiles;
+  const long long c0 = g0 / run, c1 = (g0 + tiles - 1) / run;  // the CTAs that share it
+  if (c0 == c1) return;                                        // one: it is written
+  // CTA c0 left it unfinished [2 c0 + 1], the others found it begun [2 c]
+  auto triple = [&](long long c) { return a.parts + ((2 * c + (c == c0)) * HT + h) * (D + 2); };
+  float m = -INFINITY, l = 0.f, s = 0.f;
+#pragma unroll 4
+  for (long long c = c0 + grp; c <= c1; c += GR) m = fmaxf(m, triple(c)[D]);
+#pragma unroll 4
+  for (long long c = c0 + grp; c <= c1; c += GR) {
+    const float* const p = triple(c);
+    const float w = exp2_diff(p[D], m);
+    l = fmaf(w, p[D + 1], l);
+    s = fmaf(w, p[e], s);
+  }
+  if constexpr (GR > 1) {
+    sm[grp][e] = s;
+    if (e == 0) {
+      sn[grp] = m;
+      sl[grp] = l;
+    }
+    __syncthreads();
+    if (grp) return;
+    m = -INFINITY;
+#pragma unroll
+    for (int q = 0; q < GR; ++q) m = fmaxf(m, sn[q]);
+    l = s = 0.f;
+#pragma unroll
+    for (int q = 0; q < GR; ++q) {
+      const float w = exp2_diff(sn[q], m);
+      l = fmaf(w, sl[q], l);
+      s = fmaf(w, sm[q][e], s);
+    }
+  }
+  *out = from_f32<T>(l == 0.f ? 0.f : s / l);
+}
+
+// The frame of both attention kernels: calls piece(p, rank) for what this CTA
+// has to do.  EVEN: its run of all tiles; else grid (Hkv * head_blocks * N,
+// rows), clusters of N, one whole unit a cluster.
+template <bool EVEN, int THREADS, typename F>
+__device__ __forceinline__ void paged_pieces(const PagedArgs& a, int N, F&& piece) {
+  PagedPiece p;
+  if constexpr (EVEN) {
+    __shared__ long long cum[kPagedRows + 1];
+    griddep_launch_dependents();
+    PagedRun run;
+    run.start(a, cum, THREADS);
+    while (run.next(a, &p)) piece(p, 0);
+  } else {
+    const int unit = static_cast<int>(blockIdx.x) / N;
+    p.r = blockIdx.y;
+    p.kvh = unit / a.head_blocks;
+    p.hb = unit % a.head_blocks;
+    if (!paged_row(a, p.r, blockIdx.x == 0 && threadIdx.x == 0, &p.slot, &p.first, &p.len)) return;  // the whole cluster
+    p.from = p.first / kTile;
+    p.to = (p.len + kTile - 1) / kTile;
+    p.begun = p.unfinished = false;
+    piece(p, static_cast<int>(blockIdx.x) % N);
+  }
+}
+
+// bf16.  W warps a CTA; NT column tiles of 8 query heads; TT tiles of 16 tokens
+// at a time.  The next tiles' keys are on their way while this one's weights
+// form, the next values while the next scores do; page ids are a tile ahead
+// again.
+template <int D, int NT, int W, int TT, bool EVEN>
+__global__ void __launch_bounds__(W * 32, NT == 1 ? 3 : 2) paged_bf16_kernel(PagedArgs a, int N) {
   constexpr int HT = 8 * NT, KB = D / 32, VB = D / 64;
   using bf16 = __nv_bfloat16;
   extern __shared__ float smem[];  // o [W][HT][D], ml [W][HT][2]
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, j = lane % 4;
-  const int rank = N > 1 ? static_cast<int>(cluster_rank()) : 0;
-  const int unit = static_cast<int>(blockIdx.x) / N, kvh = unit / a.head_blocks, h0 = (unit % a.head_blocks) * HT;
-  const int r = blockIdx.y;
-  int slot, first, len;
-  if (!paged_row(a, r, blockIdx.x == 0 && threadIdx.x == 0, &slot, &first, &len)) return;  // the whole cluster
-  const int* const table = a.table + static_cast<long long>(slot) * a.max_pages;
-  if (a.k_new && rank == 0 && unit % a.head_blocks == 0) store_new<bf16, D>(a, r, kvh, table, len);
+  paged_pieces<EVEN, W * 32>(a, N, [&](const PagedPiece& p, int rank) {
+    const int r = p.r, kvh = p.kvh, h0 = p.hb * HT, first = p.first, len = p.len, tiles = p.to;
+    const int* const table = a.table + static_cast<long long>(p.slot) * a.max_pages;
+    if (a.k_new && rank == 0 && p.hb == 0 && !p.unfinished) store_new<bf16, D>(a, r, kvh, table, len);
 
-  uint32_t q[NT][KB][4];
+    uint32_t q[NT][KB][4];
 #pragma unroll
-  for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int b = 0; b < KB; ++b) {
-      const int h = h0 + t * 8 + g;
-      uint4 u = make_uint4(0, 0, 0, 0);
-      if (h < a.G) u = ld16(static_cast<const bf16*>(a.q) + (static_cast<long long>(r) * a.Hkv * a.G + kvh * a.G + h) * D + b * 32 + j * 8);
-      q[t][b][0] = u.x;
-      q[t][b][1] = u.y;
-      q[t][b][2] = u.z;
-      q[t][b][3] = u.w;
-    }
-  float o[NT][VB][4][4], m[NT][2], l[NT][2];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    m[t][0] = m[t][1] = -INFINITY;
-    l[t][0] = l[t][1] = 0.f;
-#pragma unroll
-    for (int b = 0; b < VB; ++b)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) o[t][b][i][c] = 0.f;
-  }
-
-  const long long new_at = (static_cast<long long>(r) * a.Hkv + kvh) * D;
-  const int mask = (1 << a.page_shift) - 1;
-  // Rows of keys and values of position `pos` (null: not there).
-  auto rows_of = [&](int pos, const bf16** kr, const bf16** vr) {
-    *kr = *vr = nullptr;
-    if (pos < first || pos >= len) return;
-    if (a.k_new && pos == len - 1) {
-      *kr = static_cast<const bf16*>(a.k_new) + new_at;
-      *vr = static_cast<const bf16*>(a.v_new) + new_at;
-      return;
-    }
-    const long long page = page_of(a, table, pos);
-    if (page < 0) return;
-    const long long at = (((page * a.Hkv + kvh) << a.page_shift) + (pos & mask)) * D;
-    *kr = static_cast<const bf16*>(a.k_pages) + at;
-    *vr = static_cast<const bf16*>(a.v_pages) + at;
-  };
-
-  const int tile0 = first / 16, tiles = len > 0 ? (len + 15) / 16 : 0;
-  for (int tile = tile0 + (rank * W + warp) * TT; tile < tiles; tile += N * W * TT) {
-    uint4 kf[TT][2][KB], vf[TT][4][VB];
-    bool there[TT][2];  // of this lane's two score rows
-#pragma unroll
-    for (int x = 0; x < TT; ++x) {
-      const int pos = (tile + x) * 16;
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const bf16 *kr, *vr;
-        rows_of(pos + g + s * 8, &kr, &vr);
-        there[x][s] = kr != nullptr;
-#pragma unroll
-        for (int b = 0; b < KB; ++b) kf[x][s][b] = kr ? ld16(kr + b * 32 + j * 8) : make_uint4(0, 0, 0, 0);
+      for (int b = 0; b < KB; ++b) {
+        const int h = h0 + t * 8 + g;
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (h < a.G) u = ld16(static_cast<const bf16*>(a.q) + ((static_cast<long long>(r) * a.Hkv + kvh) * a.G + h) * D + b * 32 + j * 8);
+        q[t][b][0] = u.x;
+        q[t][b][1] = u.y;
+        q[t][b][2] = u.z;
+        q[t][b][3] = u.w;
       }
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const bf16 *kr, *vr;
-        rows_of(pos + 2 * j + (s & 1) + (s >> 1) * 8, &kr, &vr);
-#pragma unroll
-        for (int b = 0; b < VB; ++b) vf[x][s][b] = vr ? ld16(vr + b * 64 + g * 8) : make_uint4(0, 0, 0, 0);
-      }
-    }
+    float o[NT][VB][4][4], m[NT][2], l[NT][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      float s[TT][4];
+      m[t][0] = m[t][1] = -INFINITY;
+      l[t][0] = l[t][1] = 0.f;
+#pragma unroll
+      for (int b = 0; b < VB; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) o[t][b][i][c] = 0.f;
+    }
+
+    const bf16* const kp = static_cast<const bf16*>(a.k_pages);
+    const bf16* const vp = static_cast<const bf16*>(a.v_pages);
+    const long long new_at = (static_cast<long long>(r) * a.Hkv + kvh) * D;
+    const int mask = (1 << a.page_shift) - 1;
+    const int stop = len < tiles * kTile ? len : tiles * kTile;               // positions of the piece
+    const int old = a.k_new && stop == len ? len - 1 : stop;                  // those in the pages
+    // Page of a tile that lies whole in the old positions of one page; else -1:
+    // its rows are looked up one by one.
+    auto page_ahead = [&](int tile) {
+      if (tile * kTile < first || tile * kTile + 16 > old || a.page_shift < 4) return -1;
+      const int p = __ldg(table + (tile * kTile >> a.page_shift));
+      return p < a.pages ? p : -1;
+    };
+    auto tile_at = [&](int page, int tile) {
+      return (((static_cast<long long>(page) * a.Hkv + kvh) << a.page_shift) + (tile * kTile & mask)) * D;
+    };
+    // Element index of position `pos` in the pages, -1: not there, -2: the new token.
+    auto row_at = [&](int pos) -> long long {
+      if (pos < first || pos >= stop) return -1;
+      if (pos >= old) return -2;
+      const long long page = page_of(a, table, pos);
+      return page < 0 ? -1 : (((page * a.Hkv + kvh) << a.page_shift) + (pos & mask)) * D;
+    };
+    uint4 kf[TT][2][KB], vf[TT][4][VB];
+    unsigned there = 0;  // bit 2x + s: score row s of this lane in tile x
+    auto load_keys = [&](int tile, const int (&page)[TT]) {
+      there = 0;
 #pragma unroll
       for (int x = 0; x < TT; ++x) {
-        s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.f;
+        if (page[x] >= 0) {
+          const bf16* const p = kp + tile_at(page[x], tile + x) + g * D + j * 8;
+          there |= 3u << (2 * x);
 #pragma unroll
-        for (int b = 0; b < KB; ++b) {
-          mma16816(s[x], kf[x][0][b].x, kf[x][1][b].x, kf[x][0][b].y, kf[x][1][b].y, q[t][b][0], q[t][b][1]);
-          mma16816(s[x], kf[x][0][b].z, kf[x][1][b].z, kf[x][0][b].w, kf[x][1][b].w, q[t][b][2], q[t][b][3]);
+          for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int b = 0; b < KB; ++b) kf[x][s][b] = ld16(p + s * 8 * D + b * 32);
+        } else {
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            const long long at = row_at((tile + x) * kTile + g + s * 8);
+            const bf16* const p = at == -2 ? static_cast<const bf16*>(a.k_new) + new_at : kp + at;
+            if (at != -1) there |= 1u << (2 * x + s);
+#pragma unroll
+            for (int b = 0; b < KB; ++b) kf[x][s][b] = at != -1 ? ld16(p + b * 32 + j * 8) : make_uint4(0, 0, 0, 0);
+          }
         }
       }
-      float top[2] = {m[t][0], m[t][1]};
+    };
+    auto load_values = [&](int tile, const int (&page)[TT]) {
+#pragma unroll
+      for (int x = 0; x < TT; ++x) {
+        if (page[x] >= 0) {
+          const bf16* const p = vp + tile_at(page[x], tile + x) + 2 * j * D + g * 8;
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int b = 0; b < VB; ++b) vf[x][s][b] = ld16(p + ((s & 1) + (s >> 1) * 8) * D + b * 64);
+        } else {
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            const long long at = row_at((tile + x) * kTile + 2 * j + (s & 1) + (s >> 1) * 8);
+            const bf16* const p = at == -2 ? static_cast<const bf16*>(a.v_new) + new_at : vp + at;
+#pragma unroll
+            for (int b = 0; b < VB; ++b) vf[x][s][b] = at != -1 ? ld16(p + b * 64 + g * 8) : make_uint4(0, 0, 0, 0);
+          }
+        }
+      }
+    };
+
+    const int step = N * W * TT;
+    int tile = p.from + (rank * W + warp) * TT;
+    int page[TT], ahead[TT];
+#pragma unroll
+    for (int x = 0; x < TT; ++x) {
+      page[x] = page_ahead(tile + x);
+      ahead[x] = page_ahead(tile + step + x);
+    }
+    if (tile < tiles) {
+      load_keys(tile, page);
+      load_values(tile, page);
+    }
+    for (; tile < tiles; tile += step) {
+      float s[NT][TT][4];
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int x = 0; x < TT; ++x) {
+          s[t][x][0] = s[t][x][1] = s[t][x][2] = s[t][x][3] = 0.f;
+#pragma unroll
+          for (int b = 0; b < KB; ++b) {
+            mma16816(s[t][x], kf[x][0][b].x, kf[x][1][b].x, kf[x][0][b].y, kf[x][1][b].y, q[t][b][0], q[t][b][1]);
+            mma16816(s[t][x], kf[x][0][b].z, kf[x][1][b].z, kf[x][0][b].w, kf[x][1][b].w, q[t][b][2], q[t][b][3]);
+          }
+        }
+      const unsigned here = there;
+#pragma unroll
+      for (int x = 0; x < TT; ++x) {
+        page[x] = ahead[x];
+        ahead[x] = page_ahead(tile + 2 * step + x);
+      }
+      const bool more = tile + step < tiles;
+      if (more) load_keys(tile + step, page);
+      uint32_t w[NT][TT][2];  // weights, transposed
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float top[2] = {m[t][0], m[t][1]};
+#pragma unroll
+        for (int x = 0; x < TT; ++x)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            s[t][x][c] = here >> (2 * x + (c >> 1)) & 1 ? s[t][x][c] * a.scale : -INFINITY;
+            top[c & 1] = fmaxf(top[c & 1], s[t][x][c]);
+          }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          top[c] = fmaxf(top[c], __shfl_xor_sync(~0u, top[c], 4));
+          top[c] = fmaxf(top[c], __shfl_xor_sync(~0u, top[c], 8));
+          top[c] = fmaxf(top[c], __shfl_xor_sync(~0u, top[c], 16));
+          const float f = exp2_diff(m[t][c], top[c]);
+          m[t][c] = top[c];
+          l[t][c] *= f;
+#pragma unroll
+          for (int b = 0; b < VB; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              o[t][b][i][c] *= f;
+              o[t][b][i][c + 2] *= f;
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < TT; ++x) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            s[t][x][c] = exp2_diff(s[t][x][c], m[t][c & 1]);
+            l[t][c & 1] += s[t][x][c];
+          }
+          w[t][x][0] = transpose8x8(pack_bf16(s[t][x][0], s[t][x][1]));
+          w[t][x][1] = transpose8x8(pack_bf16(s[t][x][2], s[t][x][3]));
+        }
+      }
 #pragma unroll
       for (int x = 0; x < TT; ++x)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          s[x][c] = there[x][c >> 1] ? s[x][c] * a.scale : -INFINITY;
-          top[c & 1] = fmaxf(top[c & 1], s[x][c]);
-        }
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        top[c] = fmaxf(top[c], __shfl_xor_sync(~0u, top[c], 4));
-        top[c] = fmaxf(top[c], __shfl_xor_sync(~0u, top[c], 8));
-        top[c] = fmaxf(top[c], __shfl_xor_sync(~0u, top[c], 16));
-        const float w = exp2_diff(m[t][c], top[c]);
-        m[t][c] = top[c];
-        l[t][c] *= w;
-#pragma unroll
-        for (int b = 0; b < VB; ++b)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            o[t][b][i][c] *= w;
-            o[t][b][i][c + 2] *= w;
-          }
-      }
-#pragma unroll
-      for (int x = 0; x < TT; ++x) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          s[x][c] = exp2_diff(s[x][c], m[t][c & 1]);
-          l[t][c & 1] += s[x][c];
-        }
-        const uint32_t b0 = transpose8x8(pack_bf16(s[x][0], s[x][1])), b1 = transpose8x8(pack_bf16(s[x][2], s[x][3]));
 #pragma unroll
         for (int b = 0; b < VB; ++b) {
           const uint32_t* const v0 = reinterpret_cast<const uint32_t*>(&vf[x][0][b]);
@@ -302,135 +541,146 @@ __global__ void __launch_bounds__(W * 32) paged_bf16_kernel(PagedArgs a, int N) 
           const uint32_t* const v2 = reinterpret_cast<const uint32_t*>(&vf[x][2][b]);
           const uint32_t* const v3 = reinterpret_cast<const uint32_t*>(&vf[x][3][b]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            mma16816(o[t][b][i], __byte_perm(v0[i], v1[i], 0x5410), __byte_perm(v0[i], v1[i], 0x7632),
-                     __byte_perm(v2[i], v3[i], 0x5410), __byte_perm(v2[i], v3[i], 0x7632), b0, b1);
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t a0 = __byte_perm(v0[i], v1[i], 0x5410), a1 = __byte_perm(v0[i], v1[i], 0x7632),
+                           a2 = __byte_perm(v2[i], v3[i], 0x5410), a3 = __byte_perm(v2[i], v3[i], 0x7632);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) mma16816(o[t][b][i], a0, a1, a2, a3, w[t][x][0], w[t][x][1]);
+          }
         }
-      }
+      if (more) load_values(tile + step, page);
     }
-  }
 
-  float* const so = smem + warp * HT * D;
-  float* const ml = smem + W * HT * D;
+    if constexpr (EVEN) __syncthreads();  // the piece before is out of shared memory
+    float* const so = smem + warp * HT * D;
+    float* const ml = smem + W * HT * D;
 #pragma unroll
-  for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      float sum = l[t][c];
-      sum += __shfl_xor_sync(~0u, sum, 4);
-      sum += __shfl_xor_sync(~0u, sum, 8);
-      sum += __shfl_xor_sync(~0u, sum, 16);
-      const int h = t * 8 + 2 * j + c;
-      if (g == 0) {
-        ml[(warp * HT + h) * 2] = m[t][c];
-        ml[(warp * HT + h) * 2 + 1] = sum;
-      }
-#pragma unroll
-      for (int b = 0; b < VB; ++b)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          so[h * D + b * 64 + g * 8 + 2 * i] = o[t][b][i][c];
-          so[h * D + b * 64 + g * 8 + 2 * i + 1] = o[t][b][i][c + 2];
+      for (int c = 0; c < 2; ++c) {
+        float sum = l[t][c];
+        sum += __shfl_xor_sync(~0u, sum, 4);
+        sum += __shfl_xor_sync(~0u, sum, 8);
+        sum += __shfl_xor_sync(~0u, sum, 16);
+        const int h = t * 8 + 2 * j + c;
+        if (g == 0) {
+          ml[(warp * HT + h) * 2] = m[t][c];
+          ml[(warp * HT + h) * 2 + 1] = sum;
         }
-    }
-  join_and_store<bf16, D, HT, W, W * 32>(a, smem, ml, r, kvh, h0, N, rank);
+#pragma unroll
+        for (int b = 0; b < VB; ++b)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            so[h * D + b * 64 + g * 8 + 2 * i] = o[t][b][i][c];
+            so[h * D + b * 64 + g * 8 + 2 * i + 1] = o[t][b][i][c + 2];
+          }
+      }
+    join_and_store<bf16, D, HT, W, W * 32>(a, p, smem, ml, N, rank);
+  });
 }
 
 // fp32.  8 lanes a token, D / 8 dimensions each (4 of every 32); every group
-// of 8 lanes keeps its own triple for HT query heads.
-template <int D, int HT, int W>
-__global__ void __launch_bounds__(W * 32) paged_f32_kernel(PagedArgs a, int N) {
+// of 8 lanes keeps its own triple for HT query heads.  The next token's key and
+// value are on their way while this one's are used.
+template <int D, int HT, int W, bool EVEN>
+__global__ void __launch_bounds__(W * 32, 3) paged_f32_kernel(PagedArgs a, int N) {
   constexpr int B = D / 32, NP = W * 4;
   extern __shared__ float smem[];  // o [NP][HT][D], ml [NP][HT][2], q [HT][D]
   const int grp = threadIdx.x / 8, lane = threadIdx.x % 8;
-  const int rank = N > 1 ? static_cast<int>(cluster_rank()) : 0;
-  const int unit = static_cast<int>(blockIdx.x) / N, kvh = unit / a.head_blocks, h0 = (unit % a.head_blocks) * HT;
-  const int r = blockIdx.y;
-  int slot, first, len;
-  if (!paged_row(a, r, blockIdx.x == 0 && threadIdx.x == 0, &slot, &first, &len)) return;
-  const int* const table = a.table + static_cast<long long>(slot) * a.max_pages;
-  if (a.k_new && rank == 0 && unit % a.head_blocks == 0) store_new<float, D>(a, r, kvh, table, len);
-
   float* const ml = smem + NP * HT * D;
   float* const sq = ml + NP * HT * 2;
-  for (int e = threadIdx.x; e < HT * D; e += W * 32)
-    sq[e] = h0 + e / D < a.G
-                ? static_cast<const float*>(a.q)[(static_cast<long long>(r) * a.Hkv * a.G + kvh * a.G + h0) * D + e] * a.scale
-                : 0.f;
-  __syncthreads();
-  float o[HT][B][4], m[HT], l[HT];
-#pragma unroll
-  for (int h = 0; h < HT; ++h) {
-    m[h] = -INFINITY;
-    l[h] = 0.f;
-#pragma unroll
-    for (int b = 0; b < B; ++b)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[h][b][i] = 0.f;
-  }
-  const long long new_at = (static_cast<long long>(r) * a.Hkv + kvh) * D;
-  const int mask = (1 << a.page_shift) - 1, step = N * NP;
-  // the loop's length is the warp's, not the group's: its shuffles take every lane
-  for (int base = first + (rank * NP + grp / 4 * 4); base < len; base += step) {
-    const int pos = base + grp % 4;
-    const float *kr = nullptr, *vr = nullptr;
-    if (pos < len) {
-      if (a.k_new && pos == len - 1) {
-        kr = static_cast<const float*>(a.k_new) + new_at;
-        vr = static_cast<const float*>(a.v_new) + new_at;
-      } else {
-        const long long page = page_of(a, table, pos);
-        if (page >= 0) {
-          const long long at = (((page * a.Hkv + kvh) << a.page_shift) + (pos & mask)) * D;
-          kr = static_cast<const float*>(a.k_pages) + at;
-          vr = static_cast<const float*>(a.v_pages) + at;
-        }
-      }
-    }
-    float kf[B][4], vf[B][4];
-#pragma unroll
-    for (int b = 0; b < B; ++b) {
-      const uint4 uk = kr ? ld16(kr + b * 32 + lane * 4) : make_uint4(0, 0, 0, 0);
-      const uint4 uv = vr ? ld16(vr + b * 32 + lane * 4) : make_uint4(0, 0, 0, 0);
-      memcpy(kf[b], &uk, 16);
-      memcpy(vf[b], &uv, 16);
-    }
+  paged_pieces<EVEN, W * 32>(a, N, [&](const PagedPiece& p, int rank) {
+    const int r = p.r, kvh = p.kvh, h0 = p.hb * HT, len = p.len;
+    const int* const table = a.table + static_cast<long long>(p.slot) * a.max_pages;
+    if (a.k_new && rank == 0 && p.hb == 0 && !p.unfinished) store_new<float, D>(a, r, kvh, table, len);
+    if constexpr (EVEN) __syncthreads();  // the piece before is out of shared memory
+    for (int e = threadIdx.x; e < HT * D; e += W * 32)
+      sq[e] = h0 + e / D < a.G ? static_cast<const float*>(a.q)[((static_cast<long long>(r) * a.Hkv + kvh) * a.G + h0) * D + e] * a.scale
+                               : 0.f;
+    __syncthreads();
+    float o[HT][B][4], m[HT], l[HT];
 #pragma unroll
     for (int h = 0; h < HT; ++h) {
-      float s = 0.f;
-#pragma unroll
-      for (int b = 0; b < B; ++b) {
-        const float4 x = *reinterpret_cast<const float4*>(sq + h * D + b * 32 + lane * 4);
-        s = fmaf(kf[b][0], x.x, s);
-        s = fmaf(kf[b][1], x.y, s);
-        s = fmaf(kf[b][2], x.z, s);
-        s = fmaf(kf[b][3], x.w, s);
-      }
-      s += __shfl_xor_sync(~0u, s, 1);
-      s += __shfl_xor_sync(~0u, s, 2);
-      s += __shfl_xor_sync(~0u, s, 4);
-      if (!kr) s = -INFINITY;
-      const float top = fmaxf(m[h], s), w = exp2_diff(m[h], top), p = exp2_diff(s, top);
-      m[h] = top;
-      l[h] = fmaf(l[h], w, p);
+      m[h] = -INFINITY;
+      l[h] = 0.f;
 #pragma unroll
       for (int b = 0; b < B; ++b)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[h][b][i] = fmaf(p, vf[b][i], o[h][b][i] * w);
+        for (int i = 0; i < 4; ++i) o[h][b][i] = 0.f;
     }
-  }
+    const long long new_at = (static_cast<long long>(r) * a.Hkv + kvh) * D;
+    const int mask = (1 << a.page_shift) - 1, step = N * NP;
+    const int begin = p.first > p.from * kTile ? p.first : p.from * kTile, stop = len < p.to * kTile ? len : p.to * kTile;
+    uint4 kn[B], vn[B];
+    bool there = false;
+    auto load = [&](int pos) {
+      const float *kr = nullptr, *vr = nullptr;
+      if (pos < stop) {
+        if (a.k_new && pos == len - 1) {
+          kr = static_cast<const float*>(a.k_new) + new_at;
+          vr = static_cast<const float*>(a.v_new) + new_at;
+        } else {
+          const long long page = page_of(a, table, pos);
+          if (page >= 0) {
+            const long long at = (((page * a.Hkv + kvh) << a.page_shift) + (pos & mask)) * D;
+            kr = static_cast<const float*>(a.k_pages) + at;
+            vr = static_cast<const float*>(a.v_pages) + at;
+          }
+        }
+      }
+      there = kr != nullptr;
 #pragma unroll
-  for (int h = 0; h < HT; ++h) {
-    if (lane == 0) {
-      ml[(grp * HT + h) * 2] = m[h];
-      ml[(grp * HT + h) * 2 + 1] = l[h];
+      for (int b = 0; b < B; ++b) {
+        kn[b] = there ? ld16(kr + b * 32 + lane * 4) : make_uint4(0, 0, 0, 0);
+        vn[b] = there ? ld16(vr + b * 32 + lane * 4) : make_uint4(0, 0, 0, 0);
+      }
+    };
+    // the loop's length is the warp's, not the group's: its shuffles take every lane
+    int base = begin + rank * NP + grp / 4 * 4;
+    if (base < stop) load(base + grp % 4);
+    for (; base < stop; base += step) {
+      float kf[B][4], vf[B][4];
+      memcpy(kf, kn, sizeof kf);
+      memcpy(vf, vn, sizeof vf);
+      const bool here = there;
+      if (base + step < stop) load(base + step + grp % 4);
+#pragma unroll
+      for (int h = 0; h < HT; ++h) {
+        float s = 0.f;
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+          const float4 x = *reinterpret_cast<const float4*>(sq + h * D + b * 32 + lane * 4);
+          s = fmaf(kf[b][0], x.x, s);
+          s = fmaf(kf[b][1], x.y, s);
+          s = fmaf(kf[b][2], x.z, s);
+          s = fmaf(kf[b][3], x.w, s);
+        }
+        s += __shfl_xor_sync(~0u, s, 1);
+        s += __shfl_xor_sync(~0u, s, 2);
+        s += __shfl_xor_sync(~0u, s, 4);
+        if (!here) s = -INFINITY;
+        const float top = fmaxf(m[h], s), w = exp2_diff(m[h], top), x = exp2_diff(s, top);
+        m[h] = top;
+        l[h] = fmaf(l[h], w, x);
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[h][b][i] = fmaf(x, vf[b][i], o[h][b][i] * w);
+      }
     }
 #pragma unroll
-    for (int b = 0; b < B; ++b)
+    for (int h = 0; h < HT; ++h) {
+      if (lane == 0) {
+        ml[(grp * HT + h) * 2] = m[h];
+        ml[(grp * HT + h) * 2 + 1] = l[h];
+      }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) smem[(grp * HT + h) * D + b * 32 + lane * 4 + i] = o[h][b][i];
-  }
-  join_and_store<float, D, HT, NP, W * 32>(a, smem, ml, r, kvh, h0, N, rank);
+      for (int b = 0; b < B; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) smem[(grp * HT + h) * D + b * 32 + lane * 4 + i] = o[h][b][i];
+    }
+    join_and_store<float, D, HT, NP, W * 32>(a, p, smem, ml, N, rank);
+  });
 }
 
 // Prompts into the pages: row r's tokens [cu[r], cu[r + 1]) go to positions

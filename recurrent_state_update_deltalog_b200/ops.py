@@ -391,6 +391,13 @@ def _cache_check(x, k_pages, v_pages, block_table, heads):
     return num_pages, Hkv, page, d, block_table.shape[0], block_table.shape[1]
 
 
+@functools.lru_cache(maxsize=4096)
+def _paged_workspace(rows, Hq, Hkv, d, dt, page, max_pages, window):
+    nbytes = ctypes.c_size_t()
+    N.call("dl_paged_attention_workspace", rows, Hq, Hkv, d, dt, page, max_pages, window, ctypes.byref(nbytes))
+    return nbytes.value
+
+
 @_placed
 def paged_attention(q, k_pages, v_pages, block_table, lens, k=None, v=None, slot_idx=None, window=0, scale=None, out=None,
                     err=None):
@@ -419,9 +426,11 @@ def paged_attention(q, k_pages, v_pages, block_table, lens, k=None, v=None, slot
     _check_err(err, q.device)
     _check_cuda("q", q)
     out = torch.empty_like(q) if out is None else out
+    nbytes = _paged_workspace(rows, q.shape[1], Hkv, d, dt, page, max_pages, int(window))
+    work = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
     N.call("dl_paged_attention", _ptr(slot_idx), slots, rows, q.shape[1], Hkv, d, dt, page, num_pages, max_pages,
            _ptr(block_table), _ptr(lens), int(window), d ** -0.5 if scale is None else float(scale), _ptr(q), _ptr(k), _ptr(v),
-           _ptr(k_pages), _ptr(v_pages), _ptr(out), _ptr(err), _stream(q))
+           _ptr(k_pages), _ptr(v_pages), _ptr(out), _ptr(work), _ptr(err), _stream(q))
     return out
 
 

@@ -128,6 +128,25 @@ def test_long_rows_split_over_clusters(lens, dtype):
 
 
 @pytest.mark.parametrize("dtype", DT)
+def test_long_rows_without_a_workspace(dtype):
+    """The C call without a workspace splits less, over one cluster; the values stay within the same bounds."""
+    import ctypes
+    from recurrent_state_update_deltalog_b200 import _native as N
+    c = make([6000, 10], 1, 4, 64, 32, dtype, 10)
+    ref, bound = reference(c, 4, 0, 0.125, dtype)
+    dev = {k: c[k].cuda() for k in ("q", "kp", "vp", "table", "lens", "slot")}
+    need = ctypes.c_size_t()
+    code = 1 if dtype == torch.bfloat16 else 0
+    N.call("dl_paged_attention_workspace", 2, 4, 1, 64, code, 32, c["table"].shape[1], 0, ctypes.byref(need))
+    assert need.value > 0
+    o = torch.empty_like(dev["q"])
+    N.call("dl_paged_attention", dev["slot"].data_ptr(), 2, 2, 4, 1, 64, code, 32, dev["kp"].shape[0], c["table"].shape[1],
+           dev["table"].data_ptr(), dev["lens"].data_ptr(), 0, 0.125, dev["q"].data_ptr(), None, None, dev["kp"].data_ptr(),
+           dev["vp"].data_ptr(), o.data_ptr(), None, None, torch.cuda.current_stream().cuda_stream)
+    assert_within(o, ref, rounded(bound, ref, dtype), "o")
+
+
+@pytest.mark.parametrize("dtype", DT)
 def test_many_rows_and_a_wide_table(dtype):
     check(make([(i * 37) % 90 for i in range(260)], 4, 1, 64, 16, dtype, 5, width=64), 1, 0, dtype)
 

@@ -167,7 +167,7 @@ def test_norm_python_refusals():
 
 def paged_args(**over):
     a = dict(slot_idx=None, slots=2, rows=2, Hq=4, Hkv=2, d=64, dtype=1, page=16, pages=8, max_pages=4, table=P, lens=P,
-             window=0, scale=0.1, q=P, k=None, v=None, kp=P, vp=P, out=P, err=None)
+             window=0, scale=0.1, q=P, k=None, v=None, kp=P, vp=P, out=P, work=None, err=None)
     a.update(over)
     return list(a.values()) + [None]
 
@@ -180,7 +180,7 @@ def paged_args(**over):
     (dict(rows=65536, slots=65536), UNSUPPORTED), (dict(window=-1), ARG), (dict(scale=float("nan")), ARG),
     (dict(scale=float("inf")), ARG), (dict(table=None), ARG), (dict(lens=None), ARG), (dict(q=None), ARG), (dict(out=None), ARG),
     (dict(kp=None), ARG), (dict(k=P), ARG), (dict(v=P), ARG), (dict(q=ctypes.c_void_p(72)), ARG), (dict(lens=ODD), ARG),
-    (dict(table=ODD), ARG),
+    (dict(table=ODD), ARG), (dict(work=ODD), ARG),
 ])
 def test_paged_refusals(lib, over, status):
     assert lib.dl_paged_attention(*paged_args(**over)) == status
@@ -195,6 +195,16 @@ def test_paged_write_refusals(lib, over, status):
              starts=None, k=P, v=P, kp=P, vp=P, err=None)
     a.update(over)
     assert lib.dl_paged_write(*a.values(), None) == status
+
+
+def test_paged_workspace(lib):
+    n = ctypes.c_size_t(1)
+    assert lib.dl_paged_attention_workspace(256, 8, 8, 128, 1, 16, 32, 0, ctypes.byref(n)) == 0 and n.value == 0
+    assert lib.dl_paged_attention_workspace(1, 8, 1, 128, 1, 16, 8192, 0, ctypes.byref(n)) == 0 and n.value > 0
+    assert lib.dl_paged_attention_workspace(1, 8, 1, 128, 1, 16, 8192, 64, ctypes.byref(n)) == 0 and n.value == 0
+    assert lib.dl_paged_attention_workspace(0, 8, 1, 128, 1, 16, 8192, 0, ctypes.byref(n)) == 0 and n.value == 0
+    assert lib.dl_paged_attention_workspace(1, 8, 3, 128, 1, 16, 8, 0, ctypes.byref(n)) == ARG
+    assert lib.dl_paged_attention_workspace(1, 8, 1, 128, 1, 16, 8, 0, None) == ARG
 
 
 def test_paged_without_rows_is_a_no_op(lib):
