@@ -9,8 +9,11 @@ using dl::NormArgs;
 
 int bad(const char* msg) { return dl::record_error(DL_ERR_ARG, msg); }
 
-// How a row of n channels lies on threads: V channels a load, nv loads a
-// thread, tpr threads a row.
+constexpr int kSms = 148;
+
+// How a row of n channels lies on threads: V channels a piece (16 bytes, or
+// one channel where rows start on any address), nv pieces a thread, tpr
+// threads a row.
 struct Shape {
   int vec, nv, tpr;
   bool narrow;
@@ -18,40 +21,39 @@ struct Shape {
   int rows_per_cta() const { return narrow ? dl::kNormNarrow / tpr : 1; }
 };
 
-Shape shape_of(int n, int dtype, bool wide_loads) {
+Shape shape_of(int n, int dtype, bool aligned) {
   Shape s{};
-  s.vec = wide_loads ? (dtype == DL_BF16 ? 8 : 4) : 1;
-  const int loads = (n + s.vec - 1) / s.vec;
+  s.vec = aligned ? (dtype == DL_BF16 ? 8 : 4) : 1;
+  const int pieces = (n + s.vec - 1) / s.vec;
   s.nv = 1;
-  while (s.nv < 8 && loads > 512 * s.nv) s.nv *= 2;
-  s.narrow = loads <= 32;
+  while (s.nv < 8 && pieces > 512 * s.nv) s.nv *= 2;
+  s.narrow = pieces <= 32;
   if (s.narrow) {
     s.tpr = 8;
-    while (s.tpr < loads) s.tpr *= 2;
+    while (s.tpr < pieces) s.tpr *= 2;
   } else {
-    s.tpr = ((loads + s.nv - 1) / s.nv + 31) / 32 * 32;
+    s.tpr = ((pieces + s.nv - 1) / s.nv + 31) / 32 * 32;
   }
   return s;
 }
 
-bool wide_loads(int n, int dtype, std::initializer_list<const void*> tensors, std::initializer_list<const void*> weights) {
+// Whether every row of every tensor starts on 16 bytes, and the weights do.
+bool aligned_rows(int n, int dtype, std::initializer_list<const void*> pointers) {
   if (n % (dtype == DL_BF16 ? 8 : 4)) return false;
-  for (const void* p : tensors)
-    if (!dl::is_aligned(p, 16)) return false;
-  for (const void* p : weights)
+  for (const void* p : pointers)
     if (!dl::is_aligned(p, 16)) return false;
   return true;
 }
 
-// CTAs of the backward kernel: a few an SM, no more than there are rows.  The
-// bound is the same for every alignment, so that the workspace is too.
-int backward_ctas(long long rows, const Shape& s) {
-  const int per_sm = s.narrow ? 4 : (s.tpr > 512 ? 1 : 1024 / s.tpr > 8 ? 8 : 1024 / s.tpr);
+// CTAs of a kernel that stays and takes row after row: as many as the SMs hold
+// (by its launch bounds), no more than there are rows.
+int staying_ctas(long long rows, const Shape& s, bool back) {
+  const int per_sm = s.narrow ? (back ? 2 : 4) : (back ? 512 : 1024) / s.tpr;
   const long long need = (rows + s.rows_per_cta() - 1) / s.rows_per_cta();
-  const long long most = 148ll * per_sm;
+  const long long most = static_cast<long long>(kSms) * (per_sm < 1 ? 1 : per_sm > 8 ? 8 : per_sm);
   return static_cast<int>(need < most ? need : most);
 }
-constexpr int kMostCtas = 148 * 8;
+constexpr int kMostCtas = kSms * 8;
 
 int check(int rows, int D, int groups, int dtype, const void* y, const float* scale, const float* pre, float eps) {
   if (dtype != DL_F32 && dtype != DL_BF16) return bad("unknown dtype");
@@ -71,36 +73,64 @@ bool ok_typed(int dtype, std::initializer_list<const void*> ps) {
   return true;
 }
 
-template <typename T, int V, int NV, bool NARROW>
-cudaError_t run(const NormArgs& a, const Shape& s, int ctas, bool back, cudaStream_t st) {
+// Rows of the ring: about 100 KB an SM on their way.
+template <typename T, int NV, bool NARROW, bool GATE, bool PRE>
+cudaError_t run_ring(const NormArgs& a, const Shape& s, int ctas, bool back, cudaStream_t st) {
+  constexpr int K = 2 + GATE, KB = 2 + GATE + 2 * PRE;       // tensors read
+  constexpr int S = K * NV <= 3 ? 4 : 2, SB = KB * NV <= 5 ? 3 : 1;
+  const auto kern = back ? dl::norm_backward_ring_kernel<T, NV, NARROW, GATE, PRE, SB> : dl::norm_ring_kernel<T, NV, NARROW, GATE, PRE, S>;
+  int smem = (back ? SB * KB : S * K) * NV * 16 * s.block();
+  const int cols = back && NARROW && a.partial ? s.rows_per_cta() * a.n * 4 : 0;  // put_sums, after the last row
+  if (cols > smem) smem = cols;
+  if (smem > 40 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  kern<<<ctas, s.block(), smem, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T, int NV, bool NARROW>
+cudaError_t run_ring(const NormArgs& a, const Shape& s, int ctas, bool back, cudaStream_t st) {
+  if (a.gate) return a.pre ? run_ring<T, NV, NARROW, true, true>(a, s, ctas, back, st) : run_ring<T, NV, NARROW, true, false>(a, s, ctas, back, st);
+  return a.pre ? run_ring<T, NV, NARROW, false, true>(a, s, ctas, back, st) : run_ring<T, NV, NARROW, false, false>(a, s, ctas, back, st);
+}
+
+template <typename T, int NV, bool NARROW>
+cudaError_t run_any(const NormArgs& a, const Shape& s, int ctas, bool back, cudaStream_t st) {
   if (back) {
     const size_t smem = NARROW && a.partial ? static_cast<size_t>(s.rows_per_cta()) * a.n * 4 : 0;
-    dl::norm_backward_kernel<T, V, NV, NARROW><<<ctas, s.block(), smem, st>>>(a);
+    dl::norm_backward_kernel<T, NV, NARROW><<<ctas, s.block(), smem, st>>>(a);
   } else {
-    dl::norm_kernel<T, V, NV, NARROW><<<ctas, s.block(), 0, st>>>(a);
+    const long long all = (a.rows + s.rows_per_cta() - 1) / s.rows_per_cta();
+    dl::norm_kernel<T, NV, NARROW><<<static_cast<unsigned>(all), s.block(), 0, st>>>(a);
   }
   return cudaGetLastError();
 }
 
-template <typename T, int V>
+template <typename T>
 cudaError_t run(const NormArgs& a, const Shape& s, int ctas, bool back, cudaStream_t st) {
-  if (s.narrow) return run<T, V, 1, true>(a, s, ctas, back, st);
-  switch (s.nv) {
-    case 1: return run<T, V, 1, false>(a, s, ctas, back, st);
-    case 2: return run<T, V, 2, false>(a, s, ctas, back, st);
-    case 4:
-      if constexpr (V < 8) return run<T, V, 4, false>(a, s, ctas, back, st);
-      break;
-    default:
-      if constexpr (V < 4) return run<T, V, 8, false>(a, s, ctas, back, st);
+  if (s.vec > 1) {
+    if (s.narrow) return run_ring<T, 1, true>(a, s, ctas, back, st);
+    switch (s.nv) {
+      case 1: return run_ring<T, 1, false>(a, s, ctas, back, st);
+      case 2: return run_ring<T, 2, false>(a, s, ctas, back, st);
+      case 4:
+        if constexpr (sizeof(T) == 4) return run_ring<T, 4, false>(a, s, ctas, back, st);
+    }
+    return cudaErrorInvalidValue;
   }
-  return cudaErrorInvalidValue;
+  if (s.narrow) return run_any<T, 1, true>(a, s, ctas, back, st);
+  switch (s.nv) {
+    case 1: return run_any<T, 1, false>(a, s, ctas, back, st);
+    case 2: return run_any<T, 2, false>(a, s, ctas, back, st);
+    case 4: return run_any<T, 4, false>(a, s, ctas, back, st);
+    default: return run_any<T, 8, false>(a, s, ctas, back, st);
+  }
 }
 
 cudaError_t run(const NormArgs& a, const Shape& s, int ctas, int dtype, bool back, cudaStream_t st) {
-  if (dtype == DL_BF16)
-    return s.vec > 1 ? run<__nv_bfloat16, 8>(a, s, ctas, back, st) : run<__nv_bfloat16, 1>(a, s, ctas, back, st);
-  return s.vec > 1 ? run<float, 4>(a, s, ctas, back, st) : run<float, 1>(a, s, ctas, back, st);
+  return dtype == DL_BF16 ? run<__nv_bfloat16>(a, s, ctas, back, st) : run<float>(a, s, ctas, back, st);
 }
 
 }  // namespace
@@ -134,9 +164,9 @@ int dl_block_norm(const int* slot_idx, int slots, int rows, int D, int groups, i
   a.n = D / groups;
   a.rows = static_cast<long long>(rows) * groups;
   a.eps = eps;
-  const Shape s = shape_of(a.n, in_dtype, wide_loads(a.n, in_dtype, {y, gate, residual, out, normed}, {post_weight, scale, pre_weight}));
+  const Shape s = shape_of(a.n, in_dtype, aligned_rows(a.n, in_dtype, {y, gate, residual, out, normed, post_weight, scale, pre_weight}));
   a.tpr = s.tpr;
-  const int ctas = static_cast<int>((a.rows + s.rows_per_cta() - 1) / s.rows_per_cta());
+  const int ctas = staying_ctas(a.rows, s, false);
   const cudaError_t e = run(a, s, ctas, in_dtype, false, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? DL_OK : dl::launch_failed(e, "block norm launch");
 }
@@ -184,10 +214,9 @@ int dl_block_norm_backward(int rows, int D, int groups, int in_dtype, const void
     a.n = n;
     a.rows = static_cast<long long>(rows) * groups;
     a.eps = eps;
-    const Shape s = shape_of(n, in_dtype, wide_loads(n, in_dtype, {y, gate, residual, dout, dnormed, dy, dgate, dresidual},
-                                                     {post_weight, scale, pre_weight}));
+    const Shape s = shape_of(n, in_dtype, aligned_rows(n, in_dtype, {y, gate, residual, dout, dnormed, dy, dgate, dresidual, post_weight, scale, pre_weight}));
     a.tpr = s.tpr;
-    ctas = backward_ctas(a.rows, s);
+    ctas = staying_ctas(a.rows, s, true);
     e = run(a, s, ctas, in_dtype, true, st);
   }
   if (e == cudaSuccess && sums) {

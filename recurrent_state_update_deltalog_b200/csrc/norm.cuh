@@ -11,10 +11,15 @@
 // The backward pass forms out again from the inputs in fp32: the stored out is
 // rounded to its type, and reading residual costs what reading out would.
 //
-// Bound: memory (10 bytes an element forward, 16 backward in bf16, against
-// some 15 and 40 flops).  A row lies in the registers of one group of threads,
-// so it is read once; weights come from the L1 cache.  Narrow rows (heads)
-// share a CTA, 8 to 32 threads a row; wide rows take a CTA each.
+// Bound: memory (10 bytes an element forward, 16 backward in bf16), with the
+// instruction rate close behind (some 20 and 40 flops an element).  A row lies
+// in the registers of one group of threads, so it is read once: narrow rows
+// (heads) on 8 to 32 lanes, wide rows on a CTA.  CTAs stay and take row after
+// row: a thread's 16-byte pieces of the rows to come travel by cp.async into
+// its own places of a shared memory ring, which no other thread reads, so the
+// ring needs no barrier; weights and parameter sums stay in registers; fp32
+// operations come in pairs.  Rows that do not start on 16 bytes are read element
+// by element, one row at a time.
 #pragma once
 
 #include "ops.cuh"
@@ -79,232 +84,173 @@ __device__ __forceinline__ void row_sum(float (&v)[K], int tpr, float (*sm)[32][
   }
 }
 
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + expf(-x)); }
-
-template <typename T, int V>
-__device__ __forceinline__ Pack<T, V> load_or_zero(const void* p, long long at, bool live) {
-  if (live && p) return load_stream<T, V>(static_cast<const T*>(p) + at);
-  Pack<T, V> z;
-#pragma unroll
-  for (int j = 0; j < V; ++j) z.v[j] = from_f32<T>(0.f);
-  return z;
+// 1 / (1 + 2^(-x log2 e)), the same steps everywhere.
+__device__ __forceinline__ float sigmoid(float x) {
+  float e, s;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+  return s;
 }
 
-template <int V>
-__device__ __forceinline__ Pack<float, V> load_weight(const float* p, int c, bool live) {
-  Pack<float, V> w;
-#pragma unroll
-  for (int j = 0; j < V; ++j) w.v[j] = 1.f;
-  if (live && p) {
-    if constexpr (V % 4 == 0) {
-#pragma unroll
-      for (int j = 0; j < V; j += 4) {
-        const float4 f = __ldg(reinterpret_cast<const float4*>(p + c + j));
-        w.v[j] = f.x;
-        w.v[j + 1] = f.y;
-        w.v[j + 2] = f.z;
-        w.v[j + 3] = f.w;
-      }
+// -- rows that start on 16 bytes ---------------------------------------------------
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// 16 bytes of T as pairs.
+template <typename T>
+struct Piece {
+  static constexpr int V = 16 / sizeof(T), P = V / 2;
+  uint4 u;
+  __device__ __forceinline__ float2 pair(int i) const {
+    const uint32_t* const w = reinterpret_cast<const uint32_t*>(&u);
+    if constexpr (sizeof(T) == 4) return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    else return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  }
+  __device__ __forceinline__ void set(int i, float2 x) {
+    uint32_t* const w = reinterpret_cast<uint32_t*>(&u);
+    if constexpr (sizeof(T) == 4) {
+      w[2 * i] = __float_as_uint(x.x);
+      w[2 * i + 1] = __float_as_uint(x.y);
     } else {
-#pragma unroll
-      for (int j = 0; j < V; ++j) w.v[j] = __ldg(p + c + j);
+      const __nv_bfloat162 p = __float22bfloat162_rn(x);
+      memcpy(&w[i], &p, 4);
     }
   }
-  return w;
-}
+  __device__ __forceinline__ void store(T* p) const { __stcs(reinterpret_cast<uint4*>(p), u); }
+};
 
-// V channels a load, NV loads a thread and tensor; grid over rows (narrow: 256 / tpr rows a CTA).
-template <typename T, int V, int NV, bool NARROW>
-__global__ void __launch_bounds__(NARROW ? kNormNarrow : NV == 8 ? 1024 : 512) norm_kernel(NormArgs a) {
-  __shared__ float sm[2][32][2];
-  int turn = 0;
-  const int lane = NARROW ? static_cast<int>(threadIdx.x) % a.tpr : static_cast<int>(threadIdx.x);
-  const long long row = NARROW ? static_cast<long long>(blockIdx.x) * (kNormNarrow / a.tpr) + threadIdx.x / a.tpr
-                               : static_cast<long long>(blockIdx.x);
-  const bool here = row < a.rows && row_slot(a.slot_idx, a.slots, static_cast<int>(row / a.groups), nullptr, false) >= 0;
-  const float inv = 1.f / static_cast<float>(a.n);
-  Pack<T, V> y[NV], g[NV], x[NV];
-  bool live[NV];
+// One thread's columns of a weight vector, ones where it is absent.
+template <int NV, int V>
+struct Weights {
+  float2 v[NV][V / 2];
+  __device__ __forceinline__ void load(const float* p, int lane, int tpr, int n) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * a.tpr + lane) * V;
-    live[i] = here && c < a.n;
-    y[i] = load_or_zero<T, V>(a.y, row * a.n + c, live[i]);
-    g[i] = load_or_zero<T, V>(a.gate, row * a.n + c, live[i]);
-    x[i] = load_or_zero<T, V>(a.residual, row * a.n + c, live[i]);
-  }
-  float r1 = 1.f;
-  if (a.post) {
-    float ss[1] = {0.f};
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * tpr + lane) * V;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float f = to_f32(y[i].v[j]);
-        ss[0] = fmaf(f, f, ss[0]);
+      for (int j = 0; j < V / 4; ++j) {
+        float4 f = make_float4(1.f, 1.f, 1.f, 1.f);
+        if (p && c < n) f = __ldg(reinterpret_cast<const float4*>(p + c) + j);
+        v[i][2 * j] = make_float2(f.x, f.y);
+        v[i][2 * j + 1] = make_float2(f.z, f.w);
       }
-    row_sum<1, NARROW>(ss, a.tpr, sm, turn);
-    r1 = rsqrtf(ss[0] * inv + a.eps);
-  }
-  float o[NV][V];
-  float ss[1] = {0.f};
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * a.tpr + lane) * V;
-    const Pack<float, V> post = load_weight<V>(a.post, c, live[i]), scale = load_weight<V>(a.scale, c, live[i]);
-    Pack<T, V> w;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      float u = to_f32(y[i].v[j]) * r1 * post.v[j];
-      if (a.gate) {
-        const float q = to_f32(g[i].v[j]);
-        u *= q * sigmoid(q);
-      }
-      o[i][j] = fmaf(scale.v[j], u, to_f32(x[i].v[j]));
-      ss[0] = fmaf(o[i][j], o[i][j], ss[0]);
-      w.v[j] = from_f32<T>(o[i][j]);
     }
-    if (live[i] && a.out) store_stream<T, V>(static_cast<T*>(a.out) + row * a.n + c, w);
   }
-  if (!a.pre) return;
-  row_sum<1, NARROW>(ss, a.tpr, sm, turn);
-  const float r2 = rsqrtf(ss[0] * inv + a.eps);
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * a.tpr + lane) * V;
-    const Pack<float, V> pre = load_weight<V>(a.pre, c, live[i]);
-    Pack<T, V> w;
-#pragma unroll
-    for (int j = 0; j < V; ++j) w.v[j] = from_f32<T>(o[i][j] * r2 * pre.v[j]);
-    if (live[i]) store_stream<T, V>(static_cast<T*>(a.normed) + row * a.n + c, w);
-  }
-}
+};
 
-// A CTA takes every gridDim.x-th row (narrow: 256 / tpr rows at a time) and
-// keeps the parameter sums of its columns in registers; they end in `partial`,
-// which norm_sums_kernel adds over the CTAs in order.
-template <typename T, int V, int NV, bool NARROW>
-__global__ void __launch_bounds__(NARROW ? kNormNarrow : NV == 8 ? 1024 : 512) norm_backward_kernel(NormArgs a) {
+// This thread's places for K tensors of S rows: [S][K][NV][threads] of 16 bytes.
+template <typename T, int NV, int K, int S>
+struct NormRing {
+  static constexpr int V = 16 / sizeof(T);
+  uint4* place;
+  int threads;
+  // The places of a row's pieces, brought or (outside the row, or absent) zero.
+  __device__ __forceinline__ void issue(int s, const void* const (&src)[K], long long row, bool here, int lane, int tpr, int n) {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * tpr + lane) * V;
+        const bool live = here && c < n && src[k];
+        const T* const p = static_cast<const T*>(live ? src[k] : src[0]);
+        copy_async16(place + ((s * K + k) * NV + i) * threads, p + (live ? row * n + c : 0), live ? 16 : 0);
+      }
+    copy_commit();
+  }
+  __device__ __forceinline__ Piece<T> get(int s, int k, int i) const {
+    return {place[((s * K + k) * NV + i) * threads]};
+  }
+};
+
+template <typename T, int NV, bool NARROW, bool GATE, bool PRE, int S>
+__global__ void __launch_bounds__(NARROW ? kNormNarrow : 512, NARROW ? 4 : 2) norm_ring_kernel(NormArgs a) {
+  constexpr int V = 16 / sizeof(T), P = V / 2, K = GATE ? 3 : 2;
+  extern __shared__ __align__(16) uint4 ring_places[];
   __shared__ float sm[2][32][2];
-  extern __shared__ float cols[];  // narrow: [256 / tpr][n] of one parameter at a time
   int turn = 0;
   const int lane = NARROW ? static_cast<int>(threadIdx.x) % a.tpr : static_cast<int>(threadIdx.x);
   const int per = NARROW ? kNormNarrow / a.tpr : 1, sub = NARROW ? static_cast<int>(threadIdx.x) / a.tpr : 0;
   const float inv = 1.f / static_cast<float>(a.n);
-  float sums[3][NV][V];
+  const long long step = static_cast<long long>(gridDim.x) * per;
+  const void* src[K];
+  src[0] = a.y;
+  src[1] = a.residual;
+  if constexpr (GATE) src[2] = a.gate;
+  NormRing<T, NV, K, S> ring{ring_places + threadIdx.x, static_cast<int>(blockDim.x)};
+  auto here = [&](long long row) {
+    return row < a.rows && row_slot(a.slot_idx, a.slots, static_cast<int>(row / a.groups), nullptr, false) >= 0;
+  };
+  long long first = static_cast<long long>(blockIdx.x) * per;
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int j = 0; j < V; ++j) sums[0][i][j] = sums[1][i][j] = sums[2][i][j] = 0.f;
+  for (int s = 0; s < S; ++s) ring.issue(s, src, first + s * step + sub, here(first + s * step + sub), lane, a.tpr, a.n);
+  Weights<NV, V> post, scale, pre;
+  post.load(a.post, lane, a.tpr, a.n);
+  scale.load(a.scale, lane, a.tpr, a.n);
+  if constexpr (PRE) pre.load(a.pre, lane, a.tpr, a.n);
 
-  for (long long first = static_cast<long long>(blockIdx.x) * per; first < a.rows; first += static_cast<long long>(gridDim.x) * per) {
+  for (int s = 0; first < a.rows; first += step, s = s + 1 == S ? 0 : s + 1) {
     const long long row = first + sub;
-    Pack<T, V> y[NV], g[NV], x[NV], po[NV], pn[NV];
-    bool live[NV];
+    const bool mine = here(row);
+    copy_wait<S - 1>();
+    Piece<T> y[NV], x[NV], g[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * a.tpr + lane) * V;
-      live[i] = row < a.rows && c < a.n;
-      y[i] = load_or_zero<T, V>(a.y, row * a.n + c, live[i]);
-      g[i] = load_or_zero<T, V>(a.gate, row * a.n + c, live[i]);
-      x[i] = load_or_zero<T, V>(a.pre ? a.residual : nullptr, row * a.n + c, live[i]);
-      po[i] = load_or_zero<T, V>(a.dout, row * a.n + c, live[i]);
-      pn[i] = load_or_zero<T, V>(a.pre ? a.dnormed : nullptr, row * a.n + c, live[i]);
+      y[i] = ring.get(s, 0, i);
+      x[i] = ring.get(s, 1, i);
+      if constexpr (GATE) g[i] = ring.get(s, 2, i);
     }
+    ring.issue(s, src, row + S * step, here(row + S * step), lane, a.tpr, a.n);
     float r1 = 1.f;
     if (a.post) {
-      float ss[1] = {0.f};
+      float2 q = both(0.f);
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float f = to_f32(y[i].v[j]);
-          ss[0] = fmaf(f, f, ss[0]);
-        }
+        for (int j = 0; j < P; ++j) q = fma2(y[i].pair(j), y[i].pair(j), q);
+      float ss[1] = {q.x + q.y};
       row_sum<1, NARROW>(ss, a.tpr, sm, turn);
-      r1 = rsqrtf(ss[0] * inv + a.eps);
+      r1 = rsqrtf(fmaf(ss[0], inv, a.eps));
     }
-    float D[NV][V];  // gradient of out
-    if (a.pre) {
-      float ss[2] = {0.f, 0.f};  // out^2, d out
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (i * a.tpr + lane) * V;
-        const Pack<float, V> post = load_weight<V>(a.post, c, live[i]), scale = load_weight<V>(a.scale, c, live[i]),
-                             pre = load_weight<V>(a.pre, c, live[i]);
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          float u = to_f32(y[i].v[j]) * r1 * post.v[j];
-          if (a.gate) {
-            const float q = to_f32(g[i].v[j]);
-            u *= q * sigmoid(q);
-          }
-          D[i][j] = fmaf(scale.v[j], u, to_f32(x[i].v[j]));  // out for now
-          ss[0] = fmaf(D[i][j], D[i][j], ss[0]);
-          ss[1] = fmaf(to_f32(pn[i].v[j]) * pre.v[j], D[i][j], ss[1]);
-        }
-      }
-      row_sum<2, NARROW>(ss, a.tpr, sm, turn);
-      const float r2 = rsqrtf(ss[0] * inv + a.eps), k = ss[1] * inv * r2;  // k = mean(d on)
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const Pack<float, V> pre = load_weight<V>(a.pre, (i * a.tpr + lane) * V, live[i]);
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float on = D[i][j] * r2, dn = to_f32(pn[i].v[j]);
-          sums[2][i][j] = fmaf(dn, on, sums[2][i][j]);
-          D[i][j] = to_f32(po[i].v[j]) + r2 * (dn * pre.v[j] - on * k);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < V; ++j) D[i][j] = to_f32(po[i].v[j]);
-    }
-    float se[1] = {0.f};  // e yn
+    float2 o[NV][P], q = both(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * a.tpr + lane) * V;
-      const long long at = row * a.n + c;
-      const Pack<float, V> post = load_weight<V>(a.post, c, live[i]), scale = load_weight<V>(a.scale, c, live[i]);
-      Pack<T, V> wg, wx;
+      Piece<T> w;
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float yn = to_f32(y[i].v[j]) * r1;
-        float act = 1.f, slope = 0.f;
-        if (a.gate) {
-          const float q = to_f32(g[i].v[j]), sg = sigmoid(q);
-          act = q * sg;
-          slope = fmaf(act, 1.f - sg, sg);
+      for (int j = 0; j < P; ++j) {
+        float2 u = mul2(mul2(y[i].pair(j), both(r1)), post.v[i][j]);
+        if constexpr (GATE) {
+          const float2 f = g[i].pair(j);
+          u = mul2(u, mul2(f, make_float2(sigmoid(f.x), sigmoid(f.y))));
         }
-        wx.v[j] = from_f32<T>(D[i][j]);
-        const float Dy = D[i][j] * yn, Ds = D[i][j] * scale.v[j];
-        sums[0][i][j] = fmaf(Dy * scale.v[j], act, sums[0][i][j]);
-        sums[1][i][j] = fmaf(Dy * post.v[j], act, sums[1][i][j]);
-        wg.v[j] = from_f32<T>(Ds * post.v[j] * yn * slope);
-        D[i][j] = Ds * post.v[j] * act;  // e
-        se[0] = fmaf(D[i][j], yn, se[0]);
+        o[i][j] = fma2(scale.v[i][j], u, x[i].pair(j));
+        if constexpr (PRE) q = fma2(o[i][j], o[i][j], q);
+        w.set(j, o[i][j]);
       }
-      if (live[i] && a.dresidual) store_stream<T, V>(static_cast<T*>(a.dresidual) + at, wx);
-      if (live[i] && a.dgate) store_stream<T, V>(static_cast<T*>(a.dgate) + at, wg);
+      const int c = (i * a.tpr + lane) * V;
+      if (mine && c < a.n && a.out) w.store(static_cast<T*>(a.out) + row * a.n + c);
     }
-    if (a.dy) {
-      float k = 0.f;
-      if (a.post) {
-        row_sum<1, NARROW>(se, a.tpr, sm, turn);
-        k = se[0] * inv;
-      }
+    if constexpr (PRE) {
+      float ss[1] = {q.x + q.y};
+      row_sum<1, NARROW>(ss, a.tpr, sm, turn);
+      const float r2 = rsqrtf(fmaf(ss[0], inv, a.eps));
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        Pack<T, V> w;
+        Piece<T> w;
 #pragma unroll
-        for (int j = 0; j < V; ++j) w.v[j] = from_f32<T>(r1 * (D[i][j] - to_f32(y[i].v[j]) * r1 * k));
-        if (live[i]) store_stream<T, V>(static_cast<T*>(a.dy) + row * a.n + (i * a.tpr + lane) * V, w);
+        for (int j = 0; j < P; ++j) w.set(j, mul2(mul2(o[i][j], both(r2)), pre.v[i][j]));
+        const int c = (i * a.tpr + lane) * V;
+        if (mine && c < a.n) w.store(static_cast<T*>(a.normed) + row * a.n + c);
       }
     }
   }
-  if (!a.partial) return;
+  copy_wait<0>();
+}
+
+// A CTA's parameter sums, kept by its threads, to its part of a.partial.
+template <int NV, int V, bool NARROW>
+__device__ __forceinline__ void put_sums(const NormArgs& a, const float (&sums)[3][NV][V], float* cols, int lane, int sub, int per) {
   float* const mine = a.partial + static_cast<long long>(blockIdx.x) * 3 * a.n;
 #pragma unroll
   for (int p = 0; p < 3; ++p) {
@@ -333,6 +279,313 @@ __global__ void __launch_bounds__(NARROW ? kNormNarrow : NV == 8 ? 1024 : 512) n
         }
     }
   }
+}
+
+template <typename T, int NV, bool NARROW, bool GATE, bool PRE, int S>
+__global__ void __launch_bounds__(NARROW ? kNormNarrow : 512, NARROW ? 2 : 1) norm_backward_ring_kernel(NormArgs a) {
+  constexpr int V = 16 / sizeof(T), P = V / 2, K = 2 + GATE + 2 * PRE;
+  extern __shared__ __align__(16) uint4 ring_places[];
+  __shared__ float sm[2][32][2];
+  int turn = 0;
+  const int lane = NARROW ? static_cast<int>(threadIdx.x) % a.tpr : static_cast<int>(threadIdx.x);
+  const int per = NARROW ? kNormNarrow / a.tpr : 1, sub = NARROW ? static_cast<int>(threadIdx.x) / a.tpr : 0;
+  const float inv = 1.f / static_cast<float>(a.n);
+  const long long step = static_cast<long long>(gridDim.x) * per;
+  const void* src[K];
+  src[0] = a.y;
+  src[1] = a.dout;
+  if constexpr (GATE) src[2] = a.gate;
+  if constexpr (PRE) {
+    src[2 + GATE] = a.residual;
+    src[3 + GATE] = a.dnormed;
+  }
+  NormRing<T, NV, K, S> ring{ring_places + threadIdx.x, static_cast<int>(blockDim.x)};
+  long long first = static_cast<long long>(blockIdx.x) * per;
+#pragma unroll
+  for (int s = 0; s < S; ++s) ring.issue(s, src, first + s * step + sub, first + s * step + sub < a.rows, lane, a.tpr, a.n);
+  Weights<NV, V> post, scale, pre;
+  post.load(a.post, lane, a.tpr, a.n);
+  scale.load(a.scale, lane, a.tpr, a.n);
+  if constexpr (PRE) pre.load(a.pre, lane, a.tpr, a.n);
+  float2 sums[3][NV][P];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int j = 0; j < P; ++j) sums[0][i][j] = sums[1][i][j] = sums[2][i][j] = both(0.f);
+
+  for (int s = 0; first < a.rows; first += step, s = s + 1 == S ? 0 : s + 1) {
+    const long long row = first + sub;
+    copy_wait<S - 1>();
+    Piece<T> y[NV], po[NV], g[NV], x[NV], pn[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      y[i] = ring.get(s, 0, i);
+      po[i] = ring.get(s, 1, i);
+      if constexpr (GATE) g[i] = ring.get(s, 2, i);
+      if constexpr (PRE) {
+        x[i] = ring.get(s, 2 + GATE, i);
+        pn[i] = ring.get(s, 3 + GATE, i);
+      }
+    }
+    ring.issue(s, src, row + S * step, row + S * step < a.rows, lane, a.tpr, a.n);
+    float r1 = 1.f;
+    if (a.post) {
+      float2 q = both(0.f);
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < P; ++j) q = fma2(y[i].pair(j), y[i].pair(j), q);
+      float ss[1] = {q.x + q.y};
+      row_sum<1, NARROW>(ss, a.tpr, sm, turn);
+      r1 = rsqrtf(fmaf(ss[0], inv, a.eps));
+    }
+    float2 act[NV][P], slope[NV][P];
+    if constexpr (GATE) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+          const float2 f = g[i].pair(j), sg = make_float2(sigmoid(f.x), sigmoid(f.y));
+          act[i][j] = mul2(f, sg);
+          slope[i][j] = fma2(act[i][j], fma2(sg, both(-1.f), both(1.f)), sg);
+        }
+    }
+    float2 D[NV][P];  // gradient of out
+    if constexpr (PRE) {
+      float2 q = both(0.f), d = both(0.f);  // out^2, dnormed pre out
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+          float2 u = mul2(mul2(y[i].pair(j), both(r1)), post.v[i][j]);
+          if constexpr (GATE) u = mul2(u, act[i][j]);
+          D[i][j] = fma2(scale.v[i][j], u, x[i].pair(j));  // out for now
+          q = fma2(D[i][j], D[i][j], q);
+          d = fma2(mul2(pn[i].pair(j), pre.v[i][j]), D[i][j], d);
+        }
+      float ss[2] = {q.x + q.y, d.x + d.y};
+      row_sum<2, NARROW>(ss, a.tpr, sm, turn);
+      const float r2 = rsqrtf(fmaf(ss[0], inv, a.eps)), k = ss[1] * inv * r2;  // k = mean(d on)
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+          const float2 on = mul2(D[i][j], both(r2)), dn = pn[i].pair(j);
+          sums[2][i][j] = fma2(dn, on, sums[2][i][j]);
+          D[i][j] = fma2(both(r2), fma2(on, both(-k), mul2(dn, pre.v[i][j])), po[i].pair(j));
+        }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < P; ++j) D[i][j] = po[i].pair(j);
+    }
+    float2 q = both(0.f);  // e yn
+    const bool live_row = row < a.rows;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * a.tpr + lane) * V;
+      const bool live = live_row && c < a.n;
+      Piece<T> w;
+      if (live && a.dresidual) {
+#pragma unroll
+        for (int j = 0; j < P; ++j) w.set(j, D[i][j]);
+        w.store(static_cast<T*>(a.dresidual) + row * a.n + c);
+      }
+#pragma unroll
+      for (int j = 0; j < P; ++j) {
+        const float2 yn = mul2(y[i].pair(j), both(r1)), m = mul2(post.v[i][j], yn);
+        const float2 Ds = mul2(D[i][j], scale.v[i][j]);
+        float2 Da = D[i][j], e = Ds;
+        if constexpr (GATE) {
+          w.set(j, mul2(mul2(Ds, m), slope[i][j]));
+          Da = mul2(Da, act[i][j]);
+          e = mul2(e, act[i][j]);
+        }
+        sums[0][i][j] = fma2(e, yn, sums[0][i][j]);
+        sums[1][i][j] = fma2(Da, m, sums[1][i][j]);
+        D[i][j] = mul2(e, post.v[i][j]);  // e from here on
+        q = fma2(D[i][j], yn, q);
+      }
+      if constexpr (GATE) {
+        if (live && a.dgate) w.store(static_cast<T*>(a.dgate) + row * a.n + c);
+      }
+    }
+    if (a.dy) {
+      float k = 0.f;
+      if (a.post) {
+        float ss[1] = {q.x + q.y};
+        row_sum<1, NARROW>(ss, a.tpr, sm, turn);
+        k = ss[0] * inv * r1 * r1;  // dy = r1 e - y r1^2 mean(e yn)
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * a.tpr + lane) * V;
+        Piece<T> w;
+#pragma unroll
+        for (int j = 0; j < P; ++j) w.set(j, fma2(y[i].pair(j), both(-k), mul2(D[i][j], both(r1))));
+        if (live_row && c < a.n) w.store(static_cast<T*>(a.dy) + row * a.n + c);
+      }
+    }
+  }
+  copy_wait<0>();
+  if (!a.partial) return;
+  float flat[3][NV][V];
+#pragma unroll
+  for (int p = 0; p < 3; ++p)
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < P; ++j) {
+        flat[p][i][2 * j] = sums[p][i][j].x;
+        flat[p][i][2 * j + 1] = sums[p][i][j].y;
+      }
+  put_sums<NV, V, NARROW>(a, flat, reinterpret_cast<float*>(ring_places), lane, sub, per);
+}
+
+// -- rows on any address -------------------------------------------------------------
+
+template <typename T>
+__device__ __forceinline__ float load_or_zero(const void* p, long long at, bool live) {
+  return live && p ? to_f32(static_cast<const T*>(p)[at]) : 0.f;
+}
+
+__device__ __forceinline__ float load_weight(const float* p, int c, bool live) { return live && p ? __ldg(p + c) : 1.f; }
+
+// One channel a thread and step, NV steps.
+template <typename T, int NV, bool NARROW>
+__global__ void __launch_bounds__(NARROW ? kNormNarrow : NV == 8 ? 1024 : 512) norm_kernel(NormArgs a) {
+  __shared__ float sm[2][32][2];
+  int turn = 0;
+  const int lane = NARROW ? static_cast<int>(threadIdx.x) % a.tpr : static_cast<int>(threadIdx.x);
+  const long long row = NARROW ? static_cast<long long>(blockIdx.x) * (kNormNarrow / a.tpr) + threadIdx.x / a.tpr
+                               : static_cast<long long>(blockIdx.x);
+  const bool here = row < a.rows && row_slot(a.slot_idx, a.slots, static_cast<int>(row / a.groups), nullptr, false) >= 0;
+  const float inv = 1.f / static_cast<float>(a.n);
+  float y[NV], g[NV], o[NV], ss[1] = {0.f};
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = i * a.tpr + lane;
+    const bool live = here && c < a.n;
+    y[i] = load_or_zero<T>(a.y, row * a.n + c, live);
+    g[i] = load_or_zero<T>(a.gate, row * a.n + c, live);
+    o[i] = load_or_zero<T>(a.residual, row * a.n + c, live);
+    ss[0] = fmaf(y[i], y[i], ss[0]);
+  }
+  float r1 = 1.f;
+  if (a.post) {
+    row_sum<1, NARROW>(ss, a.tpr, sm, turn);
+    r1 = rsqrtf(fmaf(ss[0], inv, a.eps));
+  }
+  ss[0] = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = i * a.tpr + lane;
+    const bool live = here && c < a.n;
+    float u = y[i] * r1 * load_weight(a.post, c, live);
+    if (a.gate) u *= g[i] * sigmoid(g[i]);
+    o[i] = fmaf(load_weight(a.scale, c, live), u, o[i]);
+    ss[0] = fmaf(o[i], o[i], ss[0]);
+    if (live && a.out) static_cast<T*>(a.out)[row * a.n + c] = from_f32<T>(o[i]);
+  }
+  if (!a.pre) return;
+  row_sum<1, NARROW>(ss, a.tpr, sm, turn);
+  const float r2 = rsqrtf(fmaf(ss[0], inv, a.eps));
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = i * a.tpr + lane;
+    if (here && c < a.n) static_cast<T*>(a.normed)[row * a.n + c] = from_f32<T>(o[i] * r2 * load_weight(a.pre, c, true));
+  }
+}
+
+// A CTA takes every gridDim.x-th row (narrow: 256 / tpr rows at a time).
+template <typename T, int NV, bool NARROW>
+__global__ void __launch_bounds__(NARROW ? kNormNarrow : NV == 8 ? 1024 : 512) norm_backward_kernel(NormArgs a) {
+  __shared__ float sm[2][32][2];
+  extern __shared__ float cols[];  // narrow: [256 / tpr][n] of one parameter at a time
+  int turn = 0;
+  const int lane = NARROW ? static_cast<int>(threadIdx.x) % a.tpr : static_cast<int>(threadIdx.x);
+  const int per = NARROW ? kNormNarrow / a.tpr : 1, sub = NARROW ? static_cast<int>(threadIdx.x) / a.tpr : 0;
+  const float inv = 1.f / static_cast<float>(a.n);
+  float sums[3][NV][1];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) sums[0][i][0] = sums[1][i][0] = sums[2][i][0] = 0.f;
+
+  for (long long first = static_cast<long long>(blockIdx.x) * per; first < a.rows; first += static_cast<long long>(gridDim.x) * per) {
+    const long long row = first + sub;
+    float y[NV], g[NV], D[NV], pn[NV], x[NV], ss[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = i * a.tpr + lane;
+      const bool live = row < a.rows && c < a.n;
+      y[i] = load_or_zero<T>(a.y, row * a.n + c, live);
+      g[i] = load_or_zero<T>(a.gate, row * a.n + c, live);
+      D[i] = load_or_zero<T>(a.dout, row * a.n + c, live);  // gradient of out
+      x[i] = load_or_zero<T>(a.pre ? a.residual : nullptr, row * a.n + c, live);
+      pn[i] = load_or_zero<T>(a.pre ? a.dnormed : nullptr, row * a.n + c, live);
+      ss[0] = fmaf(y[i], y[i], ss[0]);
+    }
+    float r1 = 1.f;
+    if (a.post) {
+      row_sum<1, NARROW>(ss, a.tpr, sm, turn);
+      r1 = rsqrtf(fmaf(ss[0], inv, a.eps));
+    }
+    if (a.pre) {
+      float s2[2] = {0.f, 0.f};  // out^2, dnormed pre out
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = i * a.tpr + lane;
+        const bool live = row < a.rows && c < a.n;
+        float u = y[i] * r1 * load_weight(a.post, c, live);
+        if (a.gate) u *= g[i] * sigmoid(g[i]);
+        x[i] = fmaf(load_weight(a.scale, c, live), u, x[i]);  // out from here on
+        s2[0] = fmaf(x[i], x[i], s2[0]);
+        s2[1] = fmaf(pn[i] * load_weight(a.pre, c, live), x[i], s2[1]);
+      }
+      row_sum<2, NARROW>(s2, a.tpr, sm, turn);
+      const float r2 = rsqrtf(fmaf(s2[0], inv, a.eps)), k = s2[1] * inv * r2;  // k = mean(d on)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = i * a.tpr + lane;
+        const float on = x[i] * r2;
+        sums[2][i][0] = fmaf(pn[i], on, sums[2][i][0]);
+        D[i] = fmaf(r2, pn[i] * load_weight(a.pre, c, row < a.rows && c < a.n) - on * k, D[i]);
+      }
+    }
+    ss[0] = 0.f;  // e yn
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = i * a.tpr + lane;
+      const bool live = row < a.rows && c < a.n;
+      const float post = load_weight(a.post, c, live), scale = load_weight(a.scale, c, live), yn = y[i] * r1;
+      float act = 1.f, slope = 0.f;
+      if (a.gate) {
+        const float sg = sigmoid(g[i]);
+        act = g[i] * sg;
+        slope = fmaf(act, 1.f - sg, sg);
+      }
+      if (live && a.dresidual) static_cast<T*>(a.dresidual)[row * a.n + c] = from_f32<T>(D[i]);
+      const float Ds = D[i] * scale, m = post * yn;
+      sums[0][i][0] = fmaf(Ds * act, yn, sums[0][i][0]);
+      sums[1][i][0] = fmaf(D[i] * act, m, sums[1][i][0]);
+      if (live && a.dgate) static_cast<T*>(a.dgate)[row * a.n + c] = from_f32<T>(Ds * m * slope);
+      D[i] = Ds * act * post;  // e from here on
+      ss[0] = fmaf(D[i], yn, ss[0]);
+    }
+    if (a.dy) {
+      float k = 0.f;
+      if (a.post) {
+        row_sum<1, NARROW>(ss, a.tpr, sm, turn);
+        k = ss[0] * inv * r1 * r1;
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = i * a.tpr + lane;
+        if (row < a.rows && c < a.n) static_cast<T*>(a.dy)[row * a.n + c] = from_f32<T>(fmaf(y[i], -k, D[i] * r1));
+      }
+    }
+  }
+  if (a.partial) put_sums<NV, 1, NARROW>(a, sums, cols, lane, sub, per);
 }
 
 // Parameter gradients from the CTAs' sums: grid (columns / 32, 3), 32 x 32 threads.

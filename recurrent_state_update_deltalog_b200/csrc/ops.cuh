@@ -92,6 +92,16 @@ __device__ __forceinline__ int row_slot(const int* slot_idx, int slots, int r, i
   return raw;
 }
 
+// cp.async of 16 bytes of which the first `bytes` are read and the rest zeros.
+__device__ __forceinline__ void copy_async16(void* dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(gmem_u64(src)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Thread-block cluster: this CTA's rank, a barrier of all its CTAs' threads
 // (releases and acquires memory writes across the cluster), and the address of
 // the same shared memory location in CTA `rank`.

@@ -90,16 +90,6 @@ __device__ __forceinline__ float decay_of(float x) {
 // that its warp's element-wise accesses are contiguous.
 enum { WIDE = 0, SHIFT = 1, NARROW = 2 };
 
-// cp.async of 16 bytes of which the first `bytes` are read and the rest zeros.
-__device__ __forceinline__ void copy_async16(void* dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(gmem_u64(src)), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // 64 tokens by 32 * PC channels of one tensor in shared memory.
 template <typename T, int MODE, int PC>
 struct alignas(16) ScanTile {

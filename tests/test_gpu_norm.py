@@ -2,8 +2,11 @@
 
 Bounds (first order, U = 2^-24 = half an ulp of fp32, relative).  A mean over a row in fp32 is off by at most 30 U of
 the mean of its terms' magnitudes: a thread adds up to 16 terms in turn, 5 + 5 exchange steps follow, and the terms
-carry 2 to 4 roundings.  So 1 / sqrt(mean + eps) is off by 15 U, 4 U of rsqrtf and 2 U: 21 U.  The sigmoid is off by
-4 U (expf) + U + 4 U (division): 9 U, and 1 U more in q * sigmoid.  Products add 1 U a factor.  What a bound says of
+carry 2 to 4 roundings.  So 1 / sqrt(mean + eps) is off by 15 U, 4 U of rsqrtf and 2 U: 21 U.  The sigmoid of q is
+1 / (1 + e) with e = 2^fl(-q log2 e): e is off by 4 U of itself (ex2 is good to 2^-22) and by 1.5 |q| U (log2 e and
+the product are rounded, 0.5 + 1 U of an exponent of |q| log2 e, and 2^t has the slope ln 2 of itself), which reaches
+the sum by e / (1 + e) <= 1; the sum adds U and the reciprocal 2 U (1 ulp): (7 + 1.5 |q|) U, taken as a = 9 + 1.5 |q|,
+and 1 U more in q * sigmoid.  Products add 1 U a factor.  What a bound says of
 one value is carried into the next below, term by term.  A sum over R rows is off by at most R U of the sum of its
 terms' magnitudes, in any order.
 """
@@ -50,12 +53,13 @@ def reference(t, groups, eps):
         q = v["gate"]
         sg = torch.sigmoid(q)
         act, slope = q * sg, sg + q * sg * (1 - sg)
-        e_slope = 14 * U * sg + 24 * U * act.abs()
+        far = 1.5 * q.abs().clamp(max=200.0) * U          # past 200 a sigmoid is 0 or 1 either way
+        e_slope = (14 * U + far) * sg + (24 * U + 2 * far) * act.abs()
     else:
-        act, slope, e_slope = torch.ones_like(y), torch.zeros_like(y), torch.zeros_like(y)
+        act, slope, e_slope, far = torch.ones_like(y), torch.zeros_like(y), torch.zeros_like(y), 0.0
     u = scale * post * act * yn
     out = u + v.get("residual", torch.zeros_like(y))
-    e_out = 40 * U * u.abs() + U * out.abs()
+    e_out = (40 * U + far) * u.abs() + U * out.abs()
     res = {"out": (out, e_out)}
     D_, e_D = v["dout"], torch.zeros_like(y)
     if "pre_weight" in v:
@@ -76,12 +80,12 @@ def reference(t, groups, eps):
     if "residual" in v:
         res["residual"] = (D_, e_D)
     terms = D_ * act * post * yn
-    e_terms = e_D * (act * post * yn).abs() + 40 * U * terms.abs()
+    e_terms = e_D * (act * post * yn).abs() + (40 * U + far) * terms.abs()
     if "scale" in v:
         res["scale"] = (terms.sum(0), e_terms.sum(0) + rows * U * terms.abs().sum(0))
     if normed:
         p = D_ * scale * act * yn
-        e_p = e_D * (scale * act * yn).abs() + 40 * U * p.abs()
+        e_p = e_D * (scale * act * yn).abs() + (40 * U + far) * p.abs()
         fold = lambda x: x.sum(0).view(groups, D // groups).sum(0)  # noqa: E731
         res["post_weight"] = (fold(p), fold(e_p) + rows * groups * U * fold(p.abs()))
     if "gate" in v:
@@ -89,7 +93,7 @@ def reference(t, groups, eps):
         g = D_ * m * slope
         res["gate"] = (g, (D_ * m).abs() * e_slope + e_D * (m * slope).abs() + 30 * U * g.abs())
     e = D_ * scale * act * post
-    e_e = e_D * (scale * act * post).abs() + 16 * U * e.abs()
+    e_e = e_D * (scale * act * post).abs() + (16 * U + far) * e.abs()
     if normed:
         k = mean(e * yn)
         e_k = mean(e_e * yn.abs() + e.abs() * e_yn) + 32 * U * mean((e * yn).abs())
