@@ -3,7 +3,8 @@
 ``DeltaLog`` (PyTorch tensors in, CUDA library underneath), the operators of
 ``ops`` that stand beside the recurrent layers, and the raw C-ABI binding
 ``_native`` are the public surface.  Importing this package does not load the
-CUDA library; the first handle or call does, and fails loudly if it is missing.
+CUDA library; the first handle, or the first operator taken from here, does, and
+fails loudly if it is missing.
 """
 _OPS = ["gated_scan", "gated_scan_forward", "gated_scan_backward", "gated_scan_prefill", "gated_scan_step",
         "block_norm", "block_norm_backward",

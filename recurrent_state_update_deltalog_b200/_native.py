@@ -20,7 +20,7 @@ DL_PREFILL_ZERO_STATE = 1
 DL_STATIC_SCRATCH_BYTES = 16 << 20
 DL_SLOT_HOLD = 0x40000000
 DL_SCAN_CHUNK = 64
-DL_DEVERR_SLOT_INDEX, DL_DEVERR_SEQLEN, DL_DEVERR_PAGE = 2, 4, 8
+DL_DEVERR_WAIT_TIMEOUT, DL_DEVERR_SLOT_INDEX, DL_DEVERR_SEQLEN, DL_DEVERR_PAGE = 1, 2, 4, 8
 DL_OPT_STEP_KERNEL = 0
 DL_OPT_HOST_PREFETCH = 1
 DL_OPT_PDL = 2

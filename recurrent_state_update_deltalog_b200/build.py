@@ -1,8 +1,10 @@
-"""Build libdeltalog.so in-tree with nvcc for sm_100a.
+"""Build libdeltalog.so (nvcc, sm_100a) and its PyTorch face in-tree.
 
 Usage: ``python -m recurrent_state_update_deltalog_b200.build [--force] [--ptxas-v]``.
-Each .cu translation unit compiles in parallel; the shared library lands next
-to this file so that it travels with the source tree.
+Each .cu translation unit compiles in parallel; the shared libraries land next
+to this file so that they travel with the source tree.  libdeltalog.so is plain
+CUDA behind the C ABI; libdeltalog_torch.so (csrc/torch_ops.cpp, host code only)
+registers the stateless operators with the installed PyTorch and calls it.
 """
 from __future__ import annotations
 
@@ -19,6 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdeltalog.so")
+TORCH_SRC = os.path.join(CSRC, "torch_ops.cpp")
+TORCH_LIB = os.path.join(PKG, "libdeltalog_torch.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
@@ -37,17 +41,36 @@ def sources() -> list[str]:
 
 
 def _deps() -> list[str]:
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh"))]
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh", ".cpp"))]
     files.append(os.path.join(INCLUDE, "deltalog.h"))
     files.append(os.path.abspath(__file__))
     return files
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(TORCH_LIB)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(TORCH_LIB))
     return all(os.path.getmtime(f) <= t for f in _deps())
+
+
+def _build_torch_face() -> None:
+    """Compile csrc/torch_ops.cpp against the installed PyTorch; libdeltalog.so must exist."""
+    import torch
+
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    tmp = TORCH_LIB + ".tmp"
+    # the system compiler: its libstdc++ has to be the one that PyTorch has loaded
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"), "-isystem", os.path.join(cuda, "include"),
+           TORCH_SRC, "-o", tmp, LIB, "-L", os.path.join(root, "lib"), "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10",
+           "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {TORCH_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, TORCH_LIB)
 
 
 def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = True) -> str:
@@ -70,11 +93,12 @@ def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = True) 
     with ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
         objs = list(ex.map(compile_one, sources()))
     tmp = LIB + ".tmp"
-    cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
+    cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-Xlinker", "-soname=libdeltalog.so"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _build_torch_face()
     return LIB
 
 

@@ -1,0 +1,439 @@
+// PyTorch face of the stateless operators: argument checks, output and
+// workspace allocation, the current stream, and autograd.  All computation is
+// in libdeltalog, called through its C ABI.  Shapes, types, layouts and devices
+// raise ValueError here, before a pointer crosses that boundary; a status other
+// than DL_OK raises RuntimeError("<entry point> -> <status>: <message>"), which
+// the Python layer turns into DeltaLogError.
+#include <ATen/ATen.h>
+#include <c10/cuda/CUDAGuard.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/custom_function.h>
+#include <torch/csrc/autograd/functions/basic_ops.h>
+#include <torch/library.h>
+
+#include <array>
+#include <optional>
+#include <string>
+#include <tuple>
+
+#include "deltalog.h"
+
+namespace {
+
+using at::Tensor;
+using OptTensor = std::optional<Tensor>;
+using torch::autograd::AutogradContext;
+using torch::autograd::variable_list;
+
+constexpr auto F32 = at::kFloat;
+constexpr auto I32 = at::kInt;
+
+void call(const char* fn, int status) {
+  static const char* const names[] = {"DL_OK", "DL_ERR_ARG", "DL_ERR_UNSUPPORTED", "DL_ERR_CUDA", "DL_ERR_OOM", "DL_ERR_DEVICE", "DL_ERR_STATE"};
+  TORCH_CHECK(status == DL_OK, fn, " -> ", status < 0 && status >= -6 ? names[-status] : std::to_string(status).c_str(), ": ", dl_last_error());
+}
+#define DL_CALL(fn, ...) call(#fn, fn(__VA_ARGS__))
+
+std::string text(at::IntArrayRef shape) {
+  std::string s = "(";
+  for (size_t i = 0; i < shape.size(); ++i) s += (i ? ", " : "") + std::to_string(shape[i]);
+  return s + ")";
+}
+void check(const char* name, const Tensor& t, at::IntArrayRef shape, at::ScalarType dtype, at::Device device) {
+  TORCH_CHECK_VALUE(t.defined(), name, " is required");
+  TORCH_CHECK_VALUE(t.sizes() == shape, name, ": expected shape ", text(shape), ", got ", text(t.sizes()));
+  TORCH_CHECK_VALUE(t.scalar_type() == dtype, name, ": expected ", dtype, ", got ", t.scalar_type());
+  TORCH_CHECK_VALUE(t.is_contiguous(), name, " must be contiguous");
+  TORCH_CHECK_VALUE(t.device() == device, name, " must live on ", device);
+}
+void check(const char* name, const OptTensor& t, at::IntArrayRef shape, at::ScalarType dtype, at::Device device) {
+  if (t) check(name, *t, shape, dtype, device);
+}
+void check_index(const char* name, const Tensor& t, at::Device device, int64_t n = -1) {
+  TORCH_CHECK_VALUE(t.dim() == 1 && (n < 0 || t.numel() == n), name, " must be 1-D", n < 0 ? std::string() : " with " + std::to_string(n) + " entries");
+  check(name, t, t.sizes(), I32, device);
+}
+
+// The tensor that sets the type and the device of a call; its DL_* type.
+int check_first(const char* name, const Tensor& t) {
+  TORCH_CHECK_VALUE(t.scalar_type() == at::kBFloat16 || t.scalar_type() == F32, name, ": expected torch.bfloat16 or torch.float32, got ", t.scalar_type());
+  TORCH_CHECK_VALUE(t.is_contiguous(), name, " must be contiguous");
+  return t.scalar_type() == at::kBFloat16 ? DL_BF16 : DL_F32;
+}
+// Last of the checks: the device itself (all other tensors are on t's).
+void check_cuda(const char* name, const Tensor& t) { TORCH_CHECK_VALUE(t.is_cuda(), name, " must live on a CUDA device"); }
+int size_of(const char* name, int64_t n) {
+  TORCH_CHECK_VALUE(n >= 0 && n <= INT32_MAX, name, " must fit 32 bits, got ", n);
+  return static_cast<int>(n);
+}
+
+template <typename T = void>
+T* ptr(const Tensor& t) {
+  return t.defined() ? static_cast<T*>(t.data_ptr()) : nullptr;
+}
+template <typename T = void>
+T* ptr(const OptTensor& t) {
+  return t ? ptr<T>(*t) : nullptr;
+}
+void* stream_of(const Tensor& t) { return c10::cuda::getCurrentCUDAStream(t.device().index()).stream(); }
+Tensor fresh(at::IntArrayRef shape, at::ScalarType dtype, const Tensor& like) { return at::empty(shape, like.options().dtype(dtype)); }
+Tensor opt(const OptTensor& t) { return t ? *t : Tensor(); }
+OptTensor opt(const Tensor& t) { return t.defined() ? OptTensor(t) : std::nullopt; }
+// A tensor that a kernel writes in place counts as changed for autograd.
+void written(const Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+bool wants_grad(std::initializer_list<const Tensor*> ts) {
+  if (!at::GradMode::is_enabled()) return false;
+  for (const Tensor* t : ts)
+    if (t->defined() && t->requires_grad()) return true;
+  return false;
+}
+// Gradients that are constants for a second differentiation, which raises.
+variable_list once(variable_list grads) {
+  if (!at::GradMode::is_enabled()) return grads;
+  variable_list some;
+  for (const auto& g : grads)
+    if (g.defined()) some.push_back(g);
+  for (auto& g : some) g.requires_grad_(true);
+  auto raise = std::make_shared<torch::autograd::DelayedError>("this operator has no second derivative", static_cast<int64_t>(some.size()));
+  some = (*raise)(std::move(some));
+  size_t i = 0;
+  for (auto& g : grads)
+    if (g.defined()) g = some[i++];
+  return grads;
+}
+
+// -- gated linear recurrence -------------------------------------------------------
+
+struct ScanSizes {
+  int rows;
+  int64_t total, C;
+};
+
+// x [rows, T, C], or [total, C] with cu_seqlens.
+ScanSizes scan_sizes(const Tensor& x, const OptTensor& cu) {
+  if (!cu) {
+    TORCH_CHECK_VALUE(x.dim() == 3, "x must be [rows, T, C], or [total, C] with cu_seqlens");
+    return {size_of("rows", x.size(0)), x.size(0) * x.size(1), x.size(2)};
+  }
+  TORCH_CHECK_VALUE(x.dim() == 2, "x must be [total, C] with cu_seqlens");
+  check_index("cu_seqlens", *cu, x.device());
+  TORCH_CHECK_VALUE(cu->numel() >= 1, "cu_seqlens must hold rows + 1 offsets");
+  return {size_of("rows", cu->numel() - 1), x.size(0), x.size(1)};
+}
+
+std::tuple<Tensor, Tensor, Tensor> scan_forward(const Tensor& x, const Tensor& log_decay, const OptTensor& h0, const OptTensor& cu,
+                                                bool checkpoints, const OptTensor& err) {
+  const int dt = check_first("x", x);
+  const ScanSizes z = scan_sizes(x, cu);
+  check("log_decay", log_decay, x.sizes(), F32, x.device());
+  check("h0", h0, {z.rows, z.C}, F32, x.device());
+  check("err", err, {1}, I32, x.device());
+  check_cuda("x", x);
+  const c10::cuda::CUDAGuard guard(x.device());
+  Tensor h = at::empty_like(x), last = fresh({z.rows, z.C}, F32, x), ckpt;
+  if (checkpoints) ckpt = fresh({z.total / DL_SCAN_CHUNK + z.rows, z.C}, F32, x);
+  DL_CALL(dl_scan, nullptr, z.rows, z.rows, ptr<int>(cu), z.total, size_of("C", z.C), dt, ptr(x), ptr<float>(log_decay), ptr<float>(h0),
+          ptr<float>(last), ptr(h), ptr<float>(ckpt), ptr<int>(err), stream_of(x));
+  return {h, last, ckpt};
+}
+
+std::tuple<Tensor, Tensor, Tensor> scan_backward(const Tensor& x, const Tensor& log_decay, const Tensor& ckpt, const Tensor& dh,
+                                                 const OptTensor& dh_last, const OptTensor& cu, const OptTensor& err) {
+  const int dt = check_first("x", x);
+  const ScanSizes z = scan_sizes(x, cu);
+  check("log_decay", log_decay, x.sizes(), F32, x.device());
+  check("ckpt", ckpt, {z.total / DL_SCAN_CHUNK + z.rows, z.C}, F32, x.device());
+  check("dh", dh, x.sizes(), x.scalar_type(), x.device());
+  check("dh_last", dh_last, {z.rows, z.C}, F32, x.device());
+  check("err", err, {1}, I32, x.device());
+  check_cuda("x", x);
+  const c10::cuda::CUDAGuard guard(x.device());
+  Tensor dx = at::empty_like(x), dld = at::empty_like(log_decay), dh0 = fresh({z.rows, z.C}, F32, x);
+  DL_CALL(dl_scan_backward, z.rows, ptr<int>(cu), z.total, size_of("C", z.C), dt, ptr(x), ptr<float>(log_decay), ptr<float>(ckpt), ptr(dh),
+          ptr<float>(dh_last), ptr(dx), ptr<float>(dld), ptr<float>(dh0), ptr<int>(err), stream_of(x));
+  return {dx, dld, dh0};
+}
+
+struct GatedScan : torch::autograd::Function<GatedScan> {
+  static variable_list forward(AutogradContext* ctx, const Tensor& x, const Tensor& log_decay, const OptTensor& h0, const OptTensor& cu,
+                               const OptTensor& err) {
+    auto [h, last, ckpt] = scan_forward(x, log_decay, h0, cu, true, err);
+    ctx->save_for_backward({x, log_decay, ckpt, opt(cu), opt(err)});
+    ctx->saved_data["h0"] = h0 && h0->requires_grad();
+    ctx->set_materialize_grads(false);
+    return {h, last};
+  }
+  static variable_list backward(AutogradContext* ctx, variable_list g) {
+    const auto s = ctx->get_saved_variables();
+    const Tensor dh = g[0].defined() ? g[0].contiguous() : at::zeros_like(s[0]);
+    const OptTensor last = g[1].defined() ? OptTensor(g[1].contiguous()) : std::nullopt;
+    auto [dx, dld, dh0] = scan_backward(s[0], s[1], s[2], dh, last, opt(s[3]), opt(s[4]));
+    return once({dx, dld, ctx->saved_data["h0"].toBool() ? dh0 : Tensor(), Tensor(), Tensor()});
+  }
+};
+
+std::tuple<Tensor, Tensor> gated_scan(const Tensor& x, const Tensor& log_decay, const OptTensor& h0, const OptTensor& cu, const OptTensor& err) {
+  const Tensor s = opt(h0);
+  if (wants_grad({&x, &log_decay, &s})) {
+    auto out = GatedScan::apply(x, log_decay, h0, cu, err);
+    return {out[0], out[1]};
+  }
+  auto [h, last, ckpt] = scan_forward(x, log_decay, h0, cu, false, err);
+  return {h, last};
+}
+
+int check_pool(const Tensor& state, const OptTensor& new_state, int64_t C, at::Device device) {
+  TORCH_CHECK_VALUE(state.dim() == 2 && state.size(1) == C, "state must be [slots, ", C, "]");
+  check("state", state, state.sizes(), F32, device);
+  check("new_state", new_state, state.sizes(), F32, device);
+  return size_of("slots", state.size(0));
+}
+void check_slots(const OptTensor& slot_idx, int rows, int slots, at::Device device) {
+  if (slot_idx) check_index("slot_idx", *slot_idx, device, rows);
+  else TORCH_CHECK_VALUE(rows <= slots, rows, " rows without slot_idx need as many slots, got ", slots);
+}
+
+Tensor gated_scan_prefill(const Tensor& x, const Tensor& log_decay, const Tensor& state, const OptTensor& cu, const OptTensor& slot_idx,
+                          bool zero_state, const OptTensor& new_state, const OptTensor& out, const OptTensor& err) {
+  const int dt = check_first("x", x);
+  TORCH_CHECK_VALUE(cu, "cu_seqlens is required");
+  const ScanSizes z = scan_sizes(x, cu);
+  check("log_decay", log_decay, x.sizes(), F32, x.device());
+  const int slots = check_pool(state, new_state, z.C, x.device());
+  check_slots(slot_idx, z.rows, slots, x.device());
+  check("out", out, x.sizes(), x.scalar_type(), x.device());
+  check("err", err, {1}, I32, x.device());
+  check_cuda("x", x);
+  const c10::cuda::CUDAGuard guard(x.device());
+  const Tensor h = out ? *out : at::empty_like(x), to = new_state ? *new_state : state;
+  DL_CALL(dl_scan, ptr<int>(slot_idx), slots, z.rows, ptr<int>(cu), z.total, size_of("C", z.C), dt, ptr(x), ptr<float>(log_decay),
+          zero_state ? nullptr : ptr<float>(state), ptr<float>(to), ptr(h), nullptr, ptr<int>(err), stream_of(x));
+  written(to);
+  written(h);
+  return h;
+}
+
+Tensor gated_scan_step(const Tensor& x, const Tensor& log_decay, const Tensor& state, const OptTensor& slot_idx, const OptTensor& new_state,
+                       const OptTensor& out, const OptTensor& err) {
+  TORCH_CHECK_VALUE(x.dim() == 2, "x must be a tensor of 2 dimensions");
+  const int dt = check_first("x", x), rows = size_of("rows", x.size(0));
+  check("log_decay", log_decay, x.sizes(), F32, x.device());
+  const int slots = check_pool(state, new_state, x.size(1), x.device());
+  check_slots(slot_idx, rows, slots, x.device());
+  check("out", out, x.sizes(), x.scalar_type(), x.device());
+  check("err", err, {1}, I32, x.device());
+  check_cuda("x", x);
+  const c10::cuda::CUDAGuard guard(x.device());
+  const Tensor h = out ? *out : at::empty_like(x), to = new_state ? *new_state : state;
+  DL_CALL(dl_scan_step, ptr<int>(slot_idx), slots, rows, size_of("C", x.size(1)), dt, ptr(x), ptr<float>(log_decay), ptr<float>(state),
+          ptr<float>(to), ptr(h), ptr<int>(err), stream_of(x));
+  written(to);
+  written(h);
+  return h;
+}
+
+// -- norms around a block ------------------------------------------------------------
+
+struct NormSizes {
+  int dt, rows, D, groups;
+};
+
+NormSizes norm_check(const Tensor& y, const OptTensor& post, const OptTensor& gate, const OptTensor& scale, const OptTensor& residual,
+                     const OptTensor& pre, int64_t groups) {
+  const int dt = check_first("y", y);
+  TORCH_CHECK_VALUE(y.dim() >= 1, "y must have a dimension");
+  int64_t D = y.size(-1);
+  if (groups > 1 && y.dim() >= 3 && y.size(-2) == groups) D *= groups;  // [..., H, d]: the groups are a dimension
+  TORCH_CHECK_VALUE(groups >= 1 && D >= 1 && D % groups == 0, "the last dimension (", D, ") must be a positive multiple of groups (", groups, ")");
+  check("gate", gate, y.sizes(), y.scalar_type(), y.device());
+  check("residual", residual, y.sizes(), y.scalar_type(), y.device());
+  check("post_weight", post, {D / groups}, F32, y.device());
+  check("scale", scale, {D}, F32, y.device());
+  check("pre_weight", pre, {D}, F32, y.device());
+  return {dt, size_of("rows", y.numel() / D), size_of("D", D), size_of("groups", groups)};
+}
+
+std::tuple<Tensor, Tensor> norm_forward(const Tensor& y, const OptTensor& post, const OptTensor& gate, const OptTensor& scale,
+                                        const OptTensor& residual, const OptTensor& pre, int64_t groups, double eps,
+                                        const OptTensor& slot_idx, int64_t slots, const OptTensor& out, const OptTensor& normed_out) {
+  const NormSizes z = norm_check(y, post, gate, scale, residual, pre, groups);
+  if (slot_idx) check_index("slot_idx", *slot_idx, y.device(), z.rows);
+  TORCH_CHECK_VALUE(!normed_out || pre, "normed_out goes with pre_weight");
+  check("out", out, y.sizes(), y.scalar_type(), y.device());
+  check("normed_out", normed_out, y.sizes(), y.scalar_type(), y.device());
+  check_cuda("y", y);
+  const c10::cuda::CUDAGuard guard(y.device());
+  const Tensor o = out ? *out : at::empty_like(y);
+  const Tensor n = !pre ? Tensor() : normed_out ? *normed_out : at::empty_like(y);
+  DL_CALL(dl_block_norm, ptr<int>(slot_idx), size_of("slots", slots), z.rows, z.D, z.groups, z.dt, ptr(y), ptr<float>(post), ptr(gate),
+          ptr<float>(scale), ptr(residual), ptr<float>(pre), static_cast<float>(eps), ptr(o), ptr(n), stream_of(y));
+  if (out) written(o);
+  if (normed_out) written(n);
+  return {o, n};
+}
+
+using SixTensors = std::tuple<Tensor, Tensor, Tensor, Tensor, Tensor, Tensor>;
+
+// In the order y, post, gate, scale, residual, pre; bit i of `need`: wanted.
+SixTensors norm_backward(const Tensor& y, const OptTensor& dout, const OptTensor& dnormed, const OptTensor& post, const OptTensor& gate,
+                         const OptTensor& scale, const OptTensor& residual, const OptTensor& pre, int64_t groups, double eps, int64_t need) {
+  const NormSizes z = norm_check(y, post, gate, scale, residual, pre, groups);
+  TORCH_CHECK_VALUE(!dnormed || pre, "dnormed goes with pre_weight");
+  check("dout", dout, y.sizes(), y.scalar_type(), y.device());
+  check("dnormed", dnormed, y.sizes(), y.scalar_type(), y.device());
+  check_cuda("y", y);
+  const c10::cuda::CUDAGuard guard(y.device());
+  const auto like = [&](const OptTensor& t, int bit) { return t && (need >> bit & 1) ? at::empty_like(*t) : Tensor(); };
+  const Tensor dy = need & 1 ? at::empty_like(y) : Tensor(), dpost = like(post, 1), dgate = like(gate, 2), dscale = like(scale, 3),
+               dres = like(residual, 4), dpre = like(pre, 5);
+  Tensor work;
+  if (dpost.defined() || dscale.defined() || dpre.defined()) {
+    size_t bytes = 0;
+    DL_CALL(dl_block_norm_workspace, z.rows, z.D, z.groups, &bytes);
+    work = fresh({static_cast<int64_t>(bytes) + 1}, at::kByte, y);
+  }
+  DL_CALL(dl_block_norm_backward, z.rows, z.D, z.groups, z.dt, ptr(y), ptr<float>(post), ptr(gate), ptr<float>(scale), ptr(residual),
+          ptr<float>(pre), static_cast<float>(eps), ptr(dout), ptr(dnormed), ptr(dy), ptr(dgate), ptr(dres), ptr<float>(dpost),
+          ptr<float>(dscale), ptr<float>(dpre), ptr(work), stream_of(y));
+  return {dy, dpost, dgate, dscale, dres, dpre};
+}
+
+struct BlockNorm : torch::autograd::Function<BlockNorm> {
+  static variable_list forward(AutogradContext* ctx, const Tensor& y, const OptTensor& post, const OptTensor& gate, const OptTensor& scale,
+                               const OptTensor& residual, const OptTensor& pre, int64_t groups, double eps) {
+    auto [out, normed] = norm_forward(y, post, gate, scale, residual, pre, groups, eps, std::nullopt, 0, std::nullopt, std::nullopt);
+    ctx->save_for_backward({y, opt(post), opt(gate), opt(scale), opt(residual), opt(pre)});
+    int64_t need = y.requires_grad();
+    const OptTensor* const parts[] = {&post, &gate, &scale, &residual, &pre};
+    for (int i = 0; i < 5; ++i)
+      if (*parts[i] && (*parts[i])->requires_grad()) need |= 2 << i;
+    ctx->saved_data["need"] = need;
+    ctx->saved_data["groups"] = groups;
+    ctx->saved_data["eps"] = eps;
+    ctx->set_materialize_grads(false);
+    if (normed.defined()) return {out, normed};
+    return {out};
+  }
+  static variable_list backward(AutogradContext* ctx, variable_list g) {
+    const auto s = ctx->get_saved_variables();
+    const auto grad = [&](size_t i) { return i < g.size() && g[i].defined() ? OptTensor(g[i].contiguous()) : std::nullopt; };
+    auto [dy, dpost, dgate, dscale, dres, dpre] =
+        norm_backward(s[0], grad(0), grad(1), opt(s[1]), opt(s[2]), opt(s[3]), opt(s[4]), opt(s[5]), ctx->saved_data["groups"].toInt(),
+                      ctx->saved_data["eps"].toDouble(), ctx->saved_data["need"].toInt());
+    return once({dy, dpost, dgate, dscale, dres, dpre, Tensor(), Tensor()});
+  }
+};
+
+std::tuple<Tensor, Tensor> block_norm(const Tensor& y, const OptTensor& post, const OptTensor& gate, const OptTensor& scale,
+                                      const OptTensor& residual, const OptTensor& pre, int64_t groups, double eps, const OptTensor& slot_idx,
+                                      int64_t slots, const OptTensor& out, const OptTensor& normed_out) {
+  const Tensor p = opt(post), q = opt(gate), r = opt(scale), s = opt(residual), t = opt(pre);
+  if (wants_grad({&y, &p, &q, &r, &s, &t})) {
+    TORCH_CHECK_VALUE(!slot_idx && !out && !normed_out, "slot_idx, out and normed_out are for calls without gradients");
+    auto v = BlockNorm::apply(y, post, gate, scale, residual, pre, groups, eps);
+    return {v[0], v.size() > 1 ? v[1] : Tensor()};
+  }
+  return norm_forward(y, post, gate, scale, residual, pre, groups, eps, slot_idx, slots, out, normed_out);
+}
+
+// -- paged key-value cache -------------------------------------------------------------
+
+struct Cache {
+  int64_t pages;
+  int Hkv, page, d, slots, max_pages;
+};
+
+Cache cache_check(const Tensor& x, const Tensor& k_pages, const Tensor& v_pages, const Tensor& table, bool same_heads) {
+  TORCH_CHECK_VALUE(k_pages.dim() == 4, "k_pages must be [num_pages, Hkv, page_size, d]");
+  check("k_pages", k_pages, k_pages.sizes(), x.scalar_type(), x.device());
+  check("v_pages", v_pages, k_pages.sizes(), x.scalar_type(), x.device());
+  const int64_t Hkv = k_pages.size(1), d = k_pages.size(3);
+  TORCH_CHECK_VALUE(x.size(2) == d && Hkv >= 1 && x.size(1) % Hkv == 0 && (!same_heads || x.size(1) == Hkv), "heads [", x.size(1), ", ",
+                    x.size(2), "] do not fit a cache of ", Hkv, " heads of ", d);
+  TORCH_CHECK_VALUE(table.dim() == 2, "block_table must be [slots, max_pages]");
+  check("block_table", table, table.sizes(), I32, x.device());
+  return {k_pages.size(0), size_of("Hkv", Hkv), size_of("page_size", k_pages.size(2)), size_of("d", d), size_of("slots", table.size(0)),
+          size_of("max_pages", table.size(1))};
+}
+
+Tensor paged_attention(const Tensor& q, const Tensor& k_pages, const Tensor& v_pages, const Tensor& table, const Tensor& lens,
+                       const OptTensor& k, const OptTensor& v, const OptTensor& slot_idx, int64_t window, std::optional<double> scale,
+                       const OptTensor& out, const OptTensor& err) {
+  TORCH_CHECK_VALUE(q.dim() == 3, "q must be a tensor of 3 dimensions");
+  const int dt = check_first("q", q);
+  const Cache c = cache_check(q, k_pages, v_pages, table, false);
+  const int rows = size_of("rows", q.size(0)), Hq = size_of("Hq", q.size(1));
+  check_index("lens", lens, q.device(), c.slots);
+  check_slots(slot_idx, rows, c.slots, q.device());
+  TORCH_CHECK_VALUE(window >= 0 && window <= INT32_MAX, "window must be 0 (none) or a positive 32-bit number");
+  TORCH_CHECK_VALUE(k.has_value() == v.has_value(), "k and v go together");
+  check("k", k, {rows, c.Hkv, c.d}, q.scalar_type(), q.device());
+  check("v", v, {rows, c.Hkv, c.d}, q.scalar_type(), q.device());
+  check("out", out, q.sizes(), q.scalar_type(), q.device());
+  check("err", err, {1}, I32, q.device());
+  check_cuda("q", q);
+  const c10::cuda::CUDAGuard guard(q.device());
+  const Tensor o = out ? *out : at::empty_like(q);
+  size_t bytes = 0;
+  DL_CALL(dl_paged_attention_workspace, rows, Hq, c.Hkv, c.d, dt, c.page, c.max_pages, static_cast<int>(window), &bytes);
+  const Tensor work = bytes ? fresh({static_cast<int64_t>(bytes)}, at::kByte, q) : Tensor();
+  DL_CALL(dl_paged_attention, ptr<int>(slot_idx), c.slots, rows, Hq, c.Hkv, c.d, dt, c.page, c.pages, c.max_pages, ptr<int>(table),
+          ptr<int>(lens), static_cast<int>(window), scale ? static_cast<float>(*scale) : 1.f / std::sqrt(static_cast<float>(c.d)), ptr(q), ptr(k),
+          ptr(v), ptr(k_pages), ptr(v_pages), ptr(o), ptr(work), ptr<int>(err), stream_of(q));
+  if (k) {
+    written(k_pages);
+    written(v_pages);
+  }
+  if (out) written(o);
+  return o;
+}
+
+void paged_write(const Tensor& k, const Tensor& v, const Tensor& k_pages, const Tensor& v_pages, const Tensor& table, const Tensor& cu,
+                 const OptTensor& starts, const OptTensor& slot_idx, const OptTensor& err) {
+  TORCH_CHECK_VALUE(k.dim() == 3, "k must be a tensor of 3 dimensions");
+  const int dt = check_first("k", k);
+  check("v", v, k.sizes(), k.scalar_type(), k.device());
+  const Cache c = cache_check(k, k_pages, v_pages, table, true);
+  check_index("cu_seqlens", cu, k.device());
+  TORCH_CHECK_VALUE(cu.numel() >= 1, "cu_seqlens must hold rows + 1 offsets");
+  const int rows = size_of("rows", cu.numel() - 1);
+  if (starts) check_index("starts", *starts, k.device(), c.slots);
+  check_slots(slot_idx, rows, c.slots, k.device());
+  check("err", err, {1}, I32, k.device());
+  check_cuda("k", k);
+  const c10::cuda::CUDAGuard guard(k.device());
+  DL_CALL(dl_paged_write, ptr<int>(slot_idx), c.slots, rows, ptr<int>(cu), k.size(0), c.Hkv, c.d, dt, c.page, c.pages, c.max_pages,
+          ptr<int>(table), ptr<int>(starts), ptr(k), ptr(v), ptr(k_pages), ptr(v_pages), ptr<int>(err), stream_of(k));
+  written(k_pages);
+  written(v_pages);
+}
+
+}  // namespace
+
+TORCH_LIBRARY(deltalog, m) {
+  m.def("gated_scan(Tensor x, Tensor log_decay, Tensor? h0, Tensor? cu_seqlens, Tensor? err) -> (Tensor, Tensor)", gated_scan);
+  m.def("gated_scan_forward(Tensor x, Tensor log_decay, Tensor? h0, Tensor? cu_seqlens, bool checkpoints, Tensor? err) -> (Tensor, Tensor, Tensor)",
+        scan_forward);
+  m.def("gated_scan_backward(Tensor x, Tensor log_decay, Tensor ckpt, Tensor dh, Tensor? dh_last, Tensor? cu_seqlens, Tensor? err) -> "
+        "(Tensor, Tensor, Tensor)",
+        scan_backward);
+  m.def("gated_scan_prefill(Tensor x, Tensor log_decay, Tensor state, Tensor? cu_seqlens, Tensor? slot_idx, bool zero_state, "
+        "Tensor? new_state, Tensor? out, Tensor? err) -> Tensor",
+        gated_scan_prefill);
+  m.def("gated_scan_step(Tensor x, Tensor log_decay, Tensor state, Tensor? slot_idx, Tensor? new_state, Tensor? out, Tensor? err) -> Tensor",
+        gated_scan_step);
+  m.def("block_norm(Tensor y, Tensor? post_weight, Tensor? gate, Tensor? scale, Tensor? residual, Tensor? pre_weight, int groups, float eps, "
+        "Tensor? slot_idx, int slots, Tensor? out, Tensor? normed_out) -> (Tensor, Tensor)",
+        block_norm);
+  m.def("block_norm_backward(Tensor y, Tensor? dout, Tensor? dnormed, Tensor? post_weight, Tensor? gate, Tensor? scale, Tensor? residual, "
+        "Tensor? pre_weight, int groups, float eps, int need) -> (Tensor, Tensor, Tensor, Tensor, Tensor, Tensor)",
+        norm_backward);
+  m.def("paged_attention(Tensor q, Tensor k_pages, Tensor v_pages, Tensor block_table, Tensor lens, Tensor? k, Tensor? v, Tensor? slot_idx, "
+        "int window, float? scale, Tensor? out, Tensor? err) -> Tensor",
+        paged_attention);
+  m.def("paged_write(Tensor k, Tensor v, Tensor k_pages, Tensor v_pages, Tensor block_table, Tensor cu_seqlens, Tensor? starts, "
+        "Tensor? slot_idx, Tensor? err) -> ()",
+        paged_write);
+}

@@ -258,3 +258,40 @@ def test_shared_input_gradients_add_up():
     (both,) = torch.autograd.grad(out.sum(), y)
     one = torch.autograd.grad(block_norm(y, w).sum(), y)[0]
     assert torch.allclose(both, one + 1.0, rtol=1e-6, atol=1e-6)
+
+
+def test_refusals_of_the_library_reach_python():
+    from recurrent_state_update_deltalog_b200 import DeltaLogError, block_norm, paged_attention
+    y = torch.zeros(2, 8193, device="cuda")
+    with pytest.raises(DeltaLogError, match="8192") as e:
+        block_norm(y)
+    assert e.value.status == -2
+    q = torch.zeros(1, 2, 96, device="cuda")
+    kp = torch.zeros(1, 2, 16, 96, device="cuda")
+    one = torch.ones(1, dtype=torch.int32, device="cuda")
+    with pytest.raises(DeltaLogError, match="64, 128"):
+        paged_attention(q, kp, kp, one.view(1, 1), one)
+    with pytest.raises(ValueError, match="stream"):
+        block_norm(torch.zeros(2, 8), stream=torch.cuda.current_stream())
+
+
+def test_no_second_derivative_and_no_graph_without_need():
+    """Differentiating twice raises; inputs without gradients give plain outputs; a leaf used in place is noticed."""
+    from recurrent_state_update_deltalog_b200 import block_norm, gated_scan, gated_scan_step
+    x = torch.randn(2, 16, device="cuda", requires_grad=True)
+    w = torch.ones(16, device="cuda")
+    (g,) = torch.autograd.grad(block_norm(x, w).square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="second derivative"):
+        g.sum().backward()
+    s = torch.randn(1, 5, 16, device="cuda", requires_grad=True)
+    (g,) = torch.autograd.grad(gated_scan(s, torch.zeros(1, 5, 16, device="cuda"))[0].square().sum(), s, create_graph=True)
+    with pytest.raises(RuntimeError, match="second derivative"):
+        g.sum().backward()
+    assert not block_norm(x.detach(), w).requires_grad
+    with torch.no_grad():
+        assert not block_norm(x, w).requires_grad
+    pool = torch.ones(2, 16, device="cuda")
+    y = (x * pool).sum()
+    gated_scan_step(torch.zeros(2, 16, device="cuda"), torch.zeros(2, 16, device="cuda"), pool)
+    with pytest.raises(RuntimeError, match="modified by an inplace"):
+        y.backward()

@@ -64,7 +64,7 @@ def test_scan_without_rows_is_a_no_op(lib):
     assert lib.dl_scan_step(None, 1, 0, 4, 1, *[None] * 7) == 0
 
 
-def test_scan_python_refusals():
+def test_scan_python_refusals(lib):
     from recurrent_state_update_deltalog_b200 import (gated_scan, gated_scan_backward, gated_scan_forward,
                                                       gated_scan_prefill, gated_scan_step)
     x, d = torch.zeros(2, 3, 4), torch.zeros(2, 3, 4)
@@ -138,7 +138,7 @@ def test_norm_workspace(lib):
     assert lib.dl_block_norm(*norm_args(rows=0, y=None, out=None)) == 0
 
 
-def test_norm_python_refusals():
+def test_norm_python_refusals(lib):
     from recurrent_state_update_deltalog_b200 import block_norm, block_norm_backward
     y, w = torch.zeros(3, 8), torch.ones(8)
     grad = y.clone().requires_grad_()
@@ -211,7 +211,7 @@ def test_paged_without_rows_is_a_no_op(lib):
     assert lib.dl_paged_attention(*paged_args(rows=0, q=None, out=None, lens=None)) == 0
 
 
-def test_paged_python_refusals():
+def test_paged_python_refusals(lib):
     from recurrent_state_update_deltalog_b200 import paged_attention, paged_write
     q, kp, tb, ln = torch.zeros(2, 4, 64), torch.zeros(5, 2, 16, 64), torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
     k, cu = torch.zeros(2, 2, 64), torch.zeros(3, dtype=torch.int32)
