@@ -461,14 +461,16 @@ int dl_scan_step(const int* slot_idx, int slots, int rows, int C, int in_dtype, 
  * out and normed may be y, gate or residual (not each other).  Rows skipped by
  * the slot map (of `slots` slots) are not written.  D / groups <= 8192.
  * Everything between the inputs and the outputs is fp32: normed is formed
- * from the unrounded out. */
+ * from the unrounded out.  stats: NULL, or float [rows * groups][2] (8-byte
+ * aligned) that keeps both reciprocal norms for dl_block_norm_backward. */
 int dl_block_norm(const int* slot_idx, int slots, int rows, int D, int groups, int in_dtype,
                   const void* y, const float* post_weight, const void* gate, const float* scale,
                   const void* residual, const float* pre_weight, float eps, void* out, void* normed,
-                  void* stream);
+                  float* stats, void* stream);
 
-/* Backward pass of dl_block_norm (no slot map) from dout and dnormed (typed
- * [rows][D], each NULL for zeros): dy, dgate, dresidual typed [rows][D],
+/* Backward pass of dl_block_norm (no slot map) from what it left in stats for
+ * the same inputs (NULL without post_weight and pre_weight) and from dout and
+ * dnormed (typed [rows][D], each NULL for zeros): dy, dgate, dresidual typed [rows][D],
  * dpost float [D / groups], dscale, dpre float [D], each NULL if not wanted.
  * No output may overlap another tensor of the call.  The parameter gradients
  * sum over rows (and groups) in fp32 in a fixed order, through `workspace`: a
@@ -478,8 +480,8 @@ int dl_block_norm_workspace(int rows, int D, int groups, size_t* bytes);
 int dl_block_norm_backward(int rows, int D, int groups, int in_dtype, const void* y,
                            const float* post_weight, const void* gate, const float* scale,
                            const void* residual, const float* pre_weight, float eps,
-                           const void* dout, const void* dnormed, void* dy, void* dgate,
-                           void* dresidual, float* dpost, float* dscale, float* dpre,
+                           const float* stats, const void* dout, const void* dnormed, void* dy,
+                           void* dgate, void* dresidual, float* dpost, float* dscale, float* dpre,
                            void* workspace, void* stream);
 
 /* Attention of one new token over a paged key-value cache, for the attention

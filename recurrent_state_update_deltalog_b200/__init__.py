@@ -7,7 +7,7 @@ CUDA library; the first handle, or the first operator taken from here, does, and
 fails loudly if it is missing.
 """
 _OPS = ["gated_scan", "gated_scan_forward", "gated_scan_backward", "gated_scan_prefill", "gated_scan_step",
-        "block_norm", "block_norm_backward",
+        "block_norm", "block_norm_forward", "block_norm_backward",
         "paged_attention", "paged_write", "check_errors"]
 __all__ = ["DeltaLog", "DeltaLogError", "suggest_m"] + _OPS
 

@@ -64,9 +64,9 @@ SIGNATURES = {
     "dl_scan": (_I, [_P, _I, _I, _P, ctypes.c_longlong, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P]),
     "dl_scan_backward": (_I, [_I, _P, ctypes.c_longlong, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
     "dl_scan_step": (_I, [_P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P]),
-    "dl_block_norm": (_I, [_P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, ctypes.c_float, _P, _P, _P]),
+    "dl_block_norm": (_I, [_P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, ctypes.c_float, _P, _P, _P, _P]),
     "dl_block_norm_workspace": (_I, [_I, _I, _I, ctypes.POINTER(ctypes.c_size_t)]),
-    "dl_block_norm_backward": (_I, [_I, _I, _I, _I, _P, _P, _P, _P, _P, _P, ctypes.c_float] + [_P] * 10),
+    "dl_block_norm_backward": (_I, [_I, _I, _I, _I, _P, _P, _P, _P, _P, _P, ctypes.c_float] + [_P] * 11),
     "dl_paged_attention": (_I, [_P, _I, _I, _I, _I, _I, _I, _I, ctypes.c_longlong, _I, _P, _P, _I, ctypes.c_float] + [_P] * 9),
     "dl_paged_attention_workspace": (_I, [_I] * 8 + [ctypes.POINTER(ctypes.c_size_t)]),
     "dl_paged_write": (_I, [_P, _I, _I, _P, ctypes.c_longlong, _I, _I, _I, _I, ctypes.c_longlong, _I] + [_P] * 8),

@@ -139,7 +139,7 @@ extern "C" {
 
 int dl_block_norm(const int* slot_idx, int slots, int rows, int D, int groups, int in_dtype, const void* y,
                   const float* post_weight, const void* gate, const float* scale, const void* residual,
-                  const float* pre_weight, float eps, void* out, void* normed, void* stream) {
+                  const float* pre_weight, float eps, void* out, void* normed, float* stats, void* stream) {
   const int rc = check(rows, D, groups, in_dtype, y, scale, pre_weight, eps);
   if (rc != DL_OK) return rc;
   if (rows == 0) return DL_OK;
@@ -147,9 +147,10 @@ int dl_block_norm(const int* slot_idx, int slots, int rows, int D, int groups, i
   if (!out && !pre_weight) return bad("null out");
   if ((pre_weight != nullptr) != (normed != nullptr)) return bad("normed goes with a pre weight");
   if (!ok_typed(in_dtype, {y, gate, residual, out, normed}) ||
-      !ok_typed(DL_F32, {post_weight, scale, pre_weight, slot_idx}))
+      !ok_typed(DL_F32, {post_weight, scale, pre_weight, slot_idx}) || !dl::is_aligned(stats, 8))
     return bad("pointer not aligned to its element size");
   NormArgs a{};
+  a.stats = stats;
   a.y = y;
   a.gate = gate;
   a.residual = residual;
@@ -181,7 +182,7 @@ int dl_block_norm_workspace(int rows, int D, int groups, size_t* bytes) {
 
 int dl_block_norm_backward(int rows, int D, int groups, int in_dtype, const void* y, const float* post_weight,
                            const void* gate, const float* scale, const void* residual, const float* pre_weight, float eps,
-                           const void* dout, const void* dnormed, void* dy, void* dgate, void* dresidual, float* dpost,
+                           const float* stats, const void* dout, const void* dnormed, void* dy, void* dgate, void* dresidual, float* dpost,
                            float* dscale, float* dpre, void* workspace, void* stream) {
   const int rc = check(rows, D, groups, in_dtype, y, scale, pre_weight, eps);
   if (rc != DL_OK) return rc;
@@ -190,6 +191,8 @@ int dl_block_norm_backward(int rows, int D, int groups, int in_dtype, const void
   if (!ok_typed(in_dtype, {y, gate, residual, dout, dnormed, dy, dgate, dresidual}) ||
       !ok_typed(DL_F32, {post_weight, scale, pre_weight, dpost, dscale, dpre, workspace}))
     return bad("pointer not aligned to its element size");
+  if (!dl::is_aligned(stats, 8)) return bad("stats not 8-byte aligned");
+  if (rows > 0 && !stats && (post_weight || pre_weight)) return bad("null stats");
   const bool sums = dpost || dscale || dpre;
   if (sums && rows > 0 && !workspace) return bad("parameter gradients need a workspace");
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -204,6 +207,7 @@ int dl_block_norm_backward(int rows, int D, int groups, int in_dtype, const void
     a.post = post_weight;
     a.scale = scale;
     a.pre = pre_weight;
+    a.stats = const_cast<float*>(stats);
     a.dout = dout;
     a.dnormed = dnormed;
     a.dy = dy;

@@ -9,7 +9,12 @@
 //   dpre = sum over rows of dnormed on, dscale of D silu(gate) post yn,
 //   dpost of D scale silu(gate) yn.
 // The backward pass forms out again from the inputs in fp32: the stored out is
-// rounded to its type, and reading residual costs what reading out would.
+// rounded to its type, and reading residual costs what reading out would.  r1
+// and r2 it takes from the forward pass (8 bytes a row).  With u = silu(gate)
+// post yn and m = scale u, both of its means then come from sums over the same
+// pass: mean(d on) = r2 S1 / n and sum(e yn) = S2 + r2 (S3 - mean(d on) r2 S4),
+// S1 = sum d out, S2 = sum m dout, S3 = sum m d, S4 = sum m out: one exchange
+// between the threads of a row.
 //
 // Bound: memory (10 bytes an element forward, 16 backward in bf16), with the
 // instruction rate close behind (some 20 and 40 flops an element).  A row lies
@@ -43,6 +48,7 @@ struct NormArgs {
   void* dy;              // [rows][n] typed, each null if not wanted
   void* dgate;
   void* dresidual;
+  float* stats;          // [rows][2]: r1, r2 (forward: written if not null)
   float* partial;        // [CTAs][3][n]: post, scale, pre sums of the CTA's rows, or null
   const int* slot_idx;   // [rows / groups] or null: rows to skip
   int slots;
@@ -54,11 +60,36 @@ struct NormArgs {
 };
 
 // Sums K values over the threads of a row.  Narrow: `tpr` (8, 16 or 32) lanes.
-// Wide: the whole CTA, through `sm` [2][32][K], whose halves alternate between
+// Wide: the whole CTA, through `sm` [2][32][4], whose halves alternate between
 // calls so that one barrier a call is enough.
 template <int K, bool NARROW>
-__device__ __forceinline__ void row_sum(float (&v)[K], int tpr, float (*sm)[32][2], int& turn) {
-  if constexpr (NARROW) {
+__device__ __forceinline__ void row_sum(float (&v)[K], int tpr, float (*sm)[32][4], int& turn) {
+  if constexpr (!NARROW && K == 4) {
+    // four sums in the shuffles of one: halves of the warp keep two values each,
+    // quarters one, whose eighth lanes then add up
+    const int lane = threadIdx.x % 32, nw = tpr / 32;
+    const bool up = lane & 16, odd = lane & 8;
+    float a = up ? v[2] : v[0], b = up ? v[3] : v[1];
+    a += __shfl_xor_sync(~0u, up ? v[0] : v[2], 16);
+    b += __shfl_xor_sync(~0u, up ? v[1] : v[3], 16);
+    float c = odd ? b : a;
+    c += __shfl_xor_sync(~0u, odd ? a : b, 8);
+    c += __shfl_xor_sync(~0u, c, 4);
+    c += __shfl_xor_sync(~0u, c, 2);
+    c += __shfl_xor_sync(~0u, c, 1);
+    float(*s)[4] = sm[turn];
+    turn ^= 1;
+    if ((lane & 7) == 0) s[threadIdx.x / 32][lane / 8] = c;
+    __syncthreads();
+    // lane l adds value l % 4 of warps l / 4, l / 4 + 8, ...
+    c = 0.f;
+    for (int w = lane / 4; w < nw; w += 8) c += s[w][lane % 4];
+    c += __shfl_xor_sync(~0u, c, 4);
+    c += __shfl_xor_sync(~0u, c, 8);
+    c += __shfl_xor_sync(~0u, c, 16);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = __shfl_sync(~0u, c, k);
+  } else if constexpr (NARROW) {
     for (int o = tpr / 2; o > 0; o >>= 1)
 #pragma unroll
       for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(~0u, v[k], o);
@@ -69,7 +100,7 @@ __device__ __forceinline__ void row_sum(float (&v)[K], int tpr, float (*sm)[32][
       for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(~0u, v[k], o);
     const int lane = threadIdx.x % 32, nw = tpr / 32;
     if (nw == 1) return;
-    float(*s)[2] = sm[turn];
+    float(*s)[4] = sm[turn];
     turn ^= 1;
     if (lane == 0)
 #pragma unroll
@@ -146,17 +177,22 @@ struct NormRing {
   static constexpr int V = 16 / sizeof(T);
   uint4* place;
   int threads;
-  // The places of a row's pieces, brought or (outside the row, or absent) zero.
-  __device__ __forceinline__ void issue(int s, const void* const (&src)[K], long long row, bool here, int lane, int tpr, int n) {
+  const T* src[K];   // y in place of an absent tensor
+  bool present[K];
+  __device__ __forceinline__ void set(int k, const void* p, const void* y) {
+    present[k] = p != nullptr;
+    src[k] = static_cast<const T*>(p ? p : y);
+  }
+  // Starts bringing a row's pieces, or zeros (outside the row, or absent).
+  __device__ __forceinline__ void issue(int s, long long row, bool here, int lane, int tpr, int n) {
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * tpr + lane) * V;
+      const bool live = here && c < n;
+      const long long at = live ? row * n + c : 0;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (i * tpr + lane) * V;
-        const bool live = here && c < n && src[k];
-        const T* const p = static_cast<const T*>(live ? src[k] : src[0]);
-        copy_async16(place + ((s * K + k) * NV + i) * threads, p + (live ? row * n + c : 0), live ? 16 : 0);
-      }
+      for (int k = 0; k < K; ++k) copy_async16(place + ((s * K + k) * NV + i) * threads, src[k] + at, live && present[k] ? 16 : 0);
+    }
     copy_commit();
   }
   __device__ __forceinline__ Piece<T> get(int s, int k, int i) const {
@@ -168,23 +204,22 @@ template <typename T, int NV, bool NARROW, bool GATE, bool PRE, int S>
 __global__ void __launch_bounds__(NARROW ? kNormNarrow : 512, NARROW ? 4 : 2) norm_ring_kernel(NormArgs a) {
   constexpr int V = 16 / sizeof(T), P = V / 2, K = GATE ? 3 : 2;
   extern __shared__ __align__(16) uint4 ring_places[];
-  __shared__ float sm[2][32][2];
+  __shared__ float sm[2][32][4];
   int turn = 0;
   const int lane = NARROW ? static_cast<int>(threadIdx.x) % a.tpr : static_cast<int>(threadIdx.x);
   const int per = NARROW ? kNormNarrow / a.tpr : 1, sub = NARROW ? static_cast<int>(threadIdx.x) / a.tpr : 0;
   const float inv = 1.f / static_cast<float>(a.n);
   const long long step = static_cast<long long>(gridDim.x) * per;
-  const void* src[K];
-  src[0] = a.y;
-  src[1] = a.residual;
-  if constexpr (GATE) src[2] = a.gate;
   NormRing<T, NV, K, S> ring{ring_places + threadIdx.x, static_cast<int>(blockDim.x)};
+  ring.set(0, a.y, a.y);
+  ring.set(1, a.residual, a.y);
+  if constexpr (GATE) ring.set(2, a.gate, a.y);
   auto here = [&](long long row) {
     return row < a.rows && row_slot(a.slot_idx, a.slots, static_cast<int>(row / a.groups), nullptr, false) >= 0;
   };
   long long first = static_cast<long long>(blockIdx.x) * per;
 #pragma unroll
-  for (int s = 0; s < S; ++s) ring.issue(s, src, first + s * step + sub, here(first + s * step + sub), lane, a.tpr, a.n);
+  for (int s = 0; s < S; ++s) ring.issue(s, first + s * step + sub, here(first + s * step + sub), lane, a.tpr, a.n);
   Weights<NV, V> post, scale, pre;
   post.load(a.post, lane, a.tpr, a.n);
   scale.load(a.scale, lane, a.tpr, a.n);
@@ -201,8 +236,8 @@ __global__ void __launch_bounds__(NARROW ? kNormNarrow : 512, NARROW ? 4 : 2) no
       x[i] = ring.get(s, 1, i);
       if constexpr (GATE) g[i] = ring.get(s, 2, i);
     }
-    ring.issue(s, src, row + S * step, here(row + S * step), lane, a.tpr, a.n);
-    float r1 = 1.f;
+    ring.issue(s, row + S * step, here(row + S * step), lane, a.tpr, a.n);
+    float r1 = 1.f, r2 = 1.f;
     if (a.post) {
       float2 q = both(0.f);
 #pragma unroll
@@ -234,7 +269,7 @@ __global__ void __launch_bounds__(NARROW ? kNormNarrow : 512, NARROW ? 4 : 2) no
     if constexpr (PRE) {
       float ss[1] = {q.x + q.y};
       row_sum<1, NARROW>(ss, a.tpr, sm, turn);
-      const float r2 = rsqrtf(fmaf(ss[0], inv, a.eps));
+      r2 = rsqrtf(fmaf(ss[0], inv, a.eps));
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         Piece<T> w;
@@ -244,6 +279,7 @@ __global__ void __launch_bounds__(NARROW ? kNormNarrow : 512, NARROW ? 4 : 2) no
         if (mine && c < a.n) w.store(static_cast<T*>(a.normed) + row * a.n + c);
       }
     }
+    if (a.stats && mine && lane == 0) *reinterpret_cast<float2*>(a.stats + 2 * row) = make_float2(r1, r2);
   }
   copy_wait<0>();
 }
@@ -285,24 +321,27 @@ template <typename T, int NV, bool NARROW, bool GATE, bool PRE, int S>
 __global__ void __launch_bounds__(NARROW ? kNormNarrow : 512, NARROW ? 2 : 1) norm_backward_ring_kernel(NormArgs a) {
   constexpr int V = 16 / sizeof(T), P = V / 2, K = 2 + GATE + 2 * PRE;
   extern __shared__ __align__(16) uint4 ring_places[];
-  __shared__ float sm[2][32][2];
+  __shared__ float sm[2][32][4];
   int turn = 0;
   const int lane = NARROW ? static_cast<int>(threadIdx.x) % a.tpr : static_cast<int>(threadIdx.x);
   const int per = NARROW ? kNormNarrow / a.tpr : 1, sub = NARROW ? static_cast<int>(threadIdx.x) / a.tpr : 0;
   const float inv = 1.f / static_cast<float>(a.n);
   const long long step = static_cast<long long>(gridDim.x) * per;
-  const void* src[K];
-  src[0] = a.y;
-  src[1] = a.dout;
-  if constexpr (GATE) src[2] = a.gate;
-  if constexpr (PRE) {
-    src[2 + GATE] = a.residual;
-    src[3 + GATE] = a.dnormed;
-  }
   NormRing<T, NV, K, S> ring{ring_places + threadIdx.x, static_cast<int>(blockDim.x)};
+  ring.set(0, a.y, a.y);
+  ring.set(1, a.dout, a.y);
+  if constexpr (GATE) ring.set(2, a.gate, a.y);
+  if constexpr (PRE) {
+    ring.set(2 + GATE, a.residual, a.y);
+    ring.set(3 + GATE, a.dnormed, a.y);
+  }
   long long first = static_cast<long long>(blockIdx.x) * per;
 #pragma unroll
-  for (int s = 0; s < S; ++s) ring.issue(s, src, first + s * step + sub, first + s * step + sub < a.rows, lane, a.tpr, a.n);
+  for (int s = 0; s < S; ++s) ring.issue(s, first + s * step + sub, first + s * step + sub < a.rows, lane, a.tpr, a.n);
+  auto stats_of = [&](long long row) {
+    return a.stats && row < a.rows ? __ldg(reinterpret_cast<const float2*>(a.stats) + row) : both(1.f);
+  };
+  float2 ahead = stats_of(first + sub);
   Weights<NV, V> post, scale, pre;
   post.load(a.post, lane, a.tpr, a.n);
   scale.load(a.scale, lane, a.tpr, a.n);
@@ -327,105 +366,77 @@ __global__ void __launch_bounds__(NARROW ? kNormNarrow : 512, NARROW ? 2 : 1) no
         pn[i] = ring.get(s, 3 + GATE, i);
       }
     }
-    ring.issue(s, src, row + S * step, row + S * step < a.rows, lane, a.tpr, a.n);
-    float r1 = 1.f;
-    if (a.post) {
-      float2 q = both(0.f);
+    ring.issue(s, row + S * step, row + S * step < a.rows, lane, a.tpr, a.n);
+    const float r1 = ahead.x, r2 = ahead.y;
+    ahead = stats_of(row + step);
+    float2 t[NV][P], u[NV][P], slope[NV][P], D[NV][P];  // post yn, act t, silu'(gate), gradient of out
+    float2 S1 = both(0.f), S2 = both(0.f), S3 = both(0.f), S4 = both(0.f);
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < P; ++j) q = fma2(y[i].pair(j), y[i].pair(j), q);
-      float ss[1] = {q.x + q.y};
-      row_sum<1, NARROW>(ss, a.tpr, sm, turn);
-      r1 = rsqrtf(fmaf(ss[0], inv, a.eps));
-    }
-    float2 act[NV][P], slope[NV][P];
-    if constexpr (GATE) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < P; ++j) {
-          const float2 f = g[i].pair(j), sg = make_float2(sigmoid(f.x), sigmoid(f.y));
-          act[i][j] = mul2(f, sg);
-          slope[i][j] = fma2(act[i][j], fma2(sg, both(-1.f), both(1.f)), sg);
+      for (int j = 0; j < P; ++j) {
+        t[i][j] = mul2(mul2(y[i].pair(j), both(r1)), post.v[i][j]);
+        u[i][j] = t[i][j];
+        if constexpr (GATE) {
+          const float2 f = g[i].pair(j), sg = make_float2(sigmoid(f.x), sigmoid(f.y)), act = mul2(f, sg);
+          slope[i][j] = fma2(act, fma2(sg, both(-1.f), both(1.f)), sg);
+          u[i][j] = mul2(act, u[i][j]);
         }
-    }
-    float2 D[NV][P];  // gradient of out
+        const float2 m = mul2(scale.v[i][j], u[i][j]), dout = po[i].pair(j);
+        S2 = fma2(m, dout, S2);
+        if constexpr (PRE) {
+          const float2 out = fma2(scale.v[i][j], u[i][j], x[i].pair(j)), d = mul2(pn[i].pair(j), pre.v[i][j]);
+          S1 = fma2(d, out, S1);
+          S3 = fma2(m, d, S3);
+          S4 = fma2(m, out, S4);
+          D[i][j] = out;  // for now
+        } else {
+          D[i][j] = dout;
+        }
+      }
+    float k = 0.f, ky;  // mean(d on); r1^2 mean(e yn), as dy = r1 e - y ky
     if constexpr (PRE) {
-      float2 q = both(0.f), d = both(0.f);  // out^2, dnormed pre out
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < P; ++j) {
-          float2 u = mul2(mul2(y[i].pair(j), both(r1)), post.v[i][j]);
-          if constexpr (GATE) u = mul2(u, act[i][j]);
-          D[i][j] = fma2(scale.v[i][j], u, x[i].pair(j));  // out for now
-          q = fma2(D[i][j], D[i][j], q);
-          d = fma2(mul2(pn[i].pair(j), pre.v[i][j]), D[i][j], d);
-        }
-      float ss[2] = {q.x + q.y, d.x + d.y};
-      row_sum<2, NARROW>(ss, a.tpr, sm, turn);
-      const float r2 = rsqrtf(fmaf(ss[0], inv, a.eps)), k = ss[1] * inv * r2;  // k = mean(d on)
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < P; ++j) {
-          const float2 on = mul2(D[i][j], both(r2)), dn = pn[i].pair(j);
-          sums[2][i][j] = fma2(dn, on, sums[2][i][j]);
-          D[i][j] = fma2(both(r2), fma2(on, both(-k), mul2(dn, pre.v[i][j])), po[i].pair(j));
-        }
+      float v[4] = {S1.x + S1.y, S2.x + S2.y, S3.x + S3.y, S4.x + S4.y};
+      row_sum<4, NARROW>(v, a.tpr, sm, turn);
+      k = v[0] * inv * r2;
+      ky = fmaf(r2, fmaf(-k * r2, v[3], v[2]), v[1]);
     } else {
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < P; ++j) D[i][j] = po[i].pair(j);
+      float v[1] = {S2.x + S2.y};
+      if (a.post) row_sum<1, NARROW>(v, a.tpr, sm, turn);
+      ky = v[0];
     }
-    float2 q = both(0.f);  // e yn
+    ky = a.post ? ky * inv * r1 * r1 : 0.f;
     const bool live_row = row < a.rows;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * a.tpr + lane) * V;
       const bool live = live_row && c < a.n;
-      Piece<T> w;
-      if (live && a.dresidual) {
-#pragma unroll
-        for (int j = 0; j < P; ++j) w.set(j, D[i][j]);
-        w.store(static_cast<T*>(a.dresidual) + row * a.n + c);
-      }
+      const long long at = row * a.n + c;
+      Piece<T> wx, wg, wy;
 #pragma unroll
       for (int j = 0; j < P; ++j) {
-        const float2 yn = mul2(y[i].pair(j), both(r1)), m = mul2(post.v[i][j], yn);
-        const float2 Ds = mul2(D[i][j], scale.v[i][j]);
-        float2 Da = D[i][j], e = Ds;
+        if constexpr (PRE) {
+          const float2 on = mul2(D[i][j], both(r2)), dn = pn[i].pair(j);
+          sums[2][i][j] = fma2(dn, on, sums[2][i][j]);
+          D[i][j] = fma2(both(r2), fma2(on, both(-k), mul2(dn, pre.v[i][j])), po[i].pair(j));
+        }
+        wx.set(j, D[i][j]);
+        sums[1][i][j] = fma2(D[i][j], u[i][j], sums[1][i][j]);
+        const float2 Ds = mul2(D[i][j], scale.v[i][j]), yn = mul2(y[i].pair(j), both(r1));
+        float2 e = Ds;
         if constexpr (GATE) {
-          w.set(j, mul2(mul2(Ds, m), slope[i][j]));
-          Da = mul2(Da, act[i][j]);
-          e = mul2(e, act[i][j]);
+          const float2 f = g[i].pair(j);
+          wg.set(j, mul2(mul2(Ds, t[i][j]), slope[i][j]));
+          e = mul2(e, mul2(f, make_float2(sigmoid(f.x), sigmoid(f.y))));
         }
         sums[0][i][j] = fma2(e, yn, sums[0][i][j]);
-        sums[1][i][j] = fma2(Da, m, sums[1][i][j]);
-        D[i][j] = mul2(e, post.v[i][j]);  // e from here on
-        q = fma2(D[i][j], yn, q);
+        wy.set(j, fma2(y[i].pair(j), both(-ky), mul2(mul2(e, post.v[i][j]), both(r1))));
       }
+      if (live && a.dresidual) wx.store(static_cast<T*>(a.dresidual) + at);
       if constexpr (GATE) {
-        if (live && a.dgate) w.store(static_cast<T*>(a.dgate) + row * a.n + c);
+        if (live && a.dgate) wg.store(static_cast<T*>(a.dgate) + at);
       }
-    }
-    if (a.dy) {
-      float k = 0.f;
-      if (a.post) {
-        float ss[1] = {q.x + q.y};
-        row_sum<1, NARROW>(ss, a.tpr, sm, turn);
-        k = ss[0] * inv * r1 * r1;  // dy = r1 e - y r1^2 mean(e yn)
-      }
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (i * a.tpr + lane) * V;
-        Piece<T> w;
-#pragma unroll
-        for (int j = 0; j < P; ++j) w.set(j, fma2(y[i].pair(j), both(-k), mul2(D[i][j], both(r1))));
-        if (live_row && c < a.n) w.store(static_cast<T*>(a.dy) + row * a.n + c);
-      }
+      if (live && a.dy) wy.store(static_cast<T*>(a.dy) + at);
     }
   }
   copy_wait<0>();
@@ -455,7 +466,7 @@ __device__ __forceinline__ float load_weight(const float* p, int c, bool live) {
 // One channel a thread and step, NV steps.
 template <typename T, int NV, bool NARROW>
 __global__ void __launch_bounds__(NARROW ? kNormNarrow : NV == 8 ? 1024 : 512) norm_kernel(NormArgs a) {
-  __shared__ float sm[2][32][2];
+  __shared__ float sm[2][32][4];
   int turn = 0;
   const int lane = NARROW ? static_cast<int>(threadIdx.x) % a.tpr : static_cast<int>(threadIdx.x);
   const long long row = NARROW ? static_cast<long long>(blockIdx.x) * (kNormNarrow / a.tpr) + threadIdx.x / a.tpr
@@ -488,9 +499,13 @@ __global__ void __launch_bounds__(NARROW ? kNormNarrow : NV == 8 ? 1024 : 512) n
     ss[0] = fmaf(o[i], o[i], ss[0]);
     if (live && a.out) static_cast<T*>(a.out)[row * a.n + c] = from_f32<T>(o[i]);
   }
+  float r2 = 1.f;
+  if (a.pre) {
+    row_sum<1, NARROW>(ss, a.tpr, sm, turn);
+    r2 = rsqrtf(fmaf(ss[0], inv, a.eps));
+  }
+  if (a.stats && here && lane == 0) *reinterpret_cast<float2*>(a.stats + 2 * row) = make_float2(r1, r2);
   if (!a.pre) return;
-  row_sum<1, NARROW>(ss, a.tpr, sm, turn);
-  const float r2 = rsqrtf(fmaf(ss[0], inv, a.eps));
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = i * a.tpr + lane;
@@ -501,7 +516,7 @@ __global__ void __launch_bounds__(NARROW ? kNormNarrow : NV == 8 ? 1024 : 512) n
 // A CTA takes every gridDim.x-th row (narrow: 256 / tpr rows at a time).
 template <typename T, int NV, bool NARROW>
 __global__ void __launch_bounds__(NARROW ? kNormNarrow : NV == 8 ? 1024 : 512) norm_backward_kernel(NormArgs a) {
-  __shared__ float sm[2][32][2];
+  __shared__ float sm[2][32][4];
   extern __shared__ float cols[];  // narrow: [256 / tpr][n] of one parameter at a time
   int turn = 0;
   const int lane = NARROW ? static_cast<int>(threadIdx.x) % a.tpr : static_cast<int>(threadIdx.x);
@@ -513,76 +528,58 @@ __global__ void __launch_bounds__(NARROW ? kNormNarrow : NV == 8 ? 1024 : 512) n
 
   for (long long first = static_cast<long long>(blockIdx.x) * per; first < a.rows; first += static_cast<long long>(gridDim.x) * per) {
     const long long row = first + sub;
-    float y[NV], g[NV], D[NV], pn[NV], x[NV], ss[1] = {0.f};
+    float y[NV], g[NV], D[NV], pn[NV], x[NV], v[4] = {0.f, 0.f, 0.f, 0.f};  // v: S1 to S4
+    const float2 r = a.stats && row < a.rows ? __ldg(reinterpret_cast<const float2*>(a.stats) + row) : make_float2(1.f, 1.f);
+    const float r1 = r.x, r2 = r.y;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = i * a.tpr + lane;
       const bool live = row < a.rows && c < a.n;
       y[i] = load_or_zero<T>(a.y, row * a.n + c, live);
       g[i] = load_or_zero<T>(a.gate, row * a.n + c, live);
-      D[i] = load_or_zero<T>(a.dout, row * a.n + c, live);  // gradient of out
+      D[i] = load_or_zero<T>(a.dout, row * a.n + c, live);
       x[i] = load_or_zero<T>(a.pre ? a.residual : nullptr, row * a.n + c, live);
       pn[i] = load_or_zero<T>(a.pre ? a.dnormed : nullptr, row * a.n + c, live);
-      ss[0] = fmaf(y[i], y[i], ss[0]);
     }
-    float r1 = 1.f;
-    if (a.post) {
-      row_sum<1, NARROW>(ss, a.tpr, sm, turn);
-      r1 = rsqrtf(fmaf(ss[0], inv, a.eps));
-    }
-    if (a.pre) {
-      float s2[2] = {0.f, 0.f};  // out^2, dnormed pre out
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = i * a.tpr + lane;
-        const bool live = row < a.rows && c < a.n;
-        float u = y[i] * r1 * load_weight(a.post, c, live);
-        if (a.gate) u *= g[i] * sigmoid(g[i]);
-        x[i] = fmaf(load_weight(a.scale, c, live), u, x[i]);  // out from here on
-        s2[0] = fmaf(x[i], x[i], s2[0]);
-        s2[1] = fmaf(pn[i] * load_weight(a.pre, c, live), x[i], s2[1]);
-      }
-      row_sum<2, NARROW>(s2, a.tpr, sm, turn);
-      const float r2 = rsqrtf(fmaf(s2[0], inv, a.eps)), k = s2[1] * inv * r2;  // k = mean(d on)
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = i * a.tpr + lane;
-        const float on = x[i] * r2;
-        sums[2][i][0] = fmaf(pn[i], on, sums[2][i][0]);
-        D[i] = fmaf(r2, pn[i] * load_weight(a.pre, c, row < a.rows && c < a.n) - on * k, D[i]);
-      }
+    for (int i = 0; i < NV; ++i) {
+      const int c = i * a.tpr + lane;
+      const bool live = row < a.rows && c < a.n;
+      const float scale = load_weight(a.scale, c, live), d = pn[i] * load_weight(a.pre, c, live);
+      float u = y[i] * r1 * load_weight(a.post, c, live);
+      if (a.gate) u *= g[i] * sigmoid(g[i]);
+      x[i] = fmaf(scale, u, x[i]);  // out from here on
+      u *= scale;
+      v[0] = fmaf(d, x[i], v[0]);
+      v[1] = fmaf(u, D[i], v[1]);
+      v[2] = fmaf(u, d, v[2]);
+      v[3] = fmaf(u, x[i], v[3]);
     }
-    ss[0] = 0.f;  // e yn
+    if (a.post || a.pre) row_sum<4, NARROW>(v, a.tpr, sm, turn);
+    const float k = a.pre ? v[0] * inv * r2 : 0.f;  // mean(d on)
+    const float ky = a.post ? (a.pre ? fmaf(r2, fmaf(-k * r2, v[3], v[2]), v[1]) : v[1]) * inv * r1 * r1 : 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = i * a.tpr + lane;
       const bool live = row < a.rows && c < a.n;
       const float post = load_weight(a.post, c, live), scale = load_weight(a.scale, c, live), yn = y[i] * r1;
+      if (a.pre) {
+        const float on = x[i] * r2;
+        sums[2][i][0] = fmaf(pn[i], on, sums[2][i][0]);
+        D[i] = fmaf(r2, pn[i] * load_weight(a.pre, c, live) - on * k, D[i]);
+      }
       float act = 1.f, slope = 0.f;
       if (a.gate) {
         const float sg = sigmoid(g[i]);
         act = g[i] * sg;
         slope = fmaf(act, 1.f - sg, sg);
       }
-      if (live && a.dresidual) static_cast<T*>(a.dresidual)[row * a.n + c] = from_f32<T>(D[i]);
-      const float Ds = D[i] * scale, m = post * yn;
+      const float Ds = D[i] * scale, t = post * yn;
       sums[0][i][0] = fmaf(Ds * act, yn, sums[0][i][0]);
-      sums[1][i][0] = fmaf(D[i] * act, m, sums[1][i][0]);
-      if (live && a.dgate) static_cast<T*>(a.dgate)[row * a.n + c] = from_f32<T>(Ds * m * slope);
-      D[i] = Ds * act * post;  // e from here on
-      ss[0] = fmaf(D[i], yn, ss[0]);
-    }
-    if (a.dy) {
-      float k = 0.f;
-      if (a.post) {
-        row_sum<1, NARROW>(ss, a.tpr, sm, turn);
-        k = ss[0] * inv * r1 * r1;
-      }
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = i * a.tpr + lane;
-        if (row < a.rows && c < a.n) static_cast<T*>(a.dy)[row * a.n + c] = from_f32<T>(fmaf(y[i], -k, D[i] * r1));
-      }
+      sums[1][i][0] = fmaf(D[i] * act, t, sums[1][i][0]);
+      if (live && a.dresidual) static_cast<T*>(a.dresidual)[row * a.n + c] = from_f32<T>(D[i]);
+      if (live && a.dgate) static_cast<T*>(a.dgate)[row * a.n + c] = from_f32<T>(Ds * t * slope);
+      if (live && a.dy) static_cast<T*>(a.dy)[row * a.n + c] = from_f32<T>(fmaf(y[i], -ky, Ds * act * post * r1));
     }
   }
   if (a.partial) put_sums<NV, 1, NARROW>(a, sums, cols, lane, sub, per);

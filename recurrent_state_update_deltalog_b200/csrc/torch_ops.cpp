@@ -255,9 +255,9 @@ NormSizes norm_check(const Tensor& y, const OptTensor& post, const OptTensor& ga
   return {dt, size_of("rows", y.numel() / D), size_of("D", D), size_of("groups", groups)};
 }
 
-std::tuple<Tensor, Tensor> norm_forward(const Tensor& y, const OptTensor& post, const OptTensor& gate, const OptTensor& scale,
+std::tuple<Tensor, Tensor, Tensor> norm_run(const Tensor& y, const OptTensor& post, const OptTensor& gate, const OptTensor& scale,
                                         const OptTensor& residual, const OptTensor& pre, int64_t groups, double eps,
-                                        const OptTensor& slot_idx, int64_t slots, const OptTensor& out, const OptTensor& normed_out) {
+                                        const OptTensor& slot_idx, int64_t slots, const OptTensor& out, const OptTensor& normed_out, bool stats) {
   const NormSizes z = norm_check(y, post, gate, scale, residual, pre, groups);
   if (slot_idx) check_index("slot_idx", *slot_idx, y.device(), z.rows);
   TORCH_CHECK_VALUE(!normed_out || pre, "normed_out goes with pre_weight");
@@ -267,20 +267,23 @@ std::tuple<Tensor, Tensor> norm_forward(const Tensor& y, const OptTensor& post, 
   const c10::cuda::CUDAGuard guard(y.device());
   const Tensor o = out ? *out : at::empty_like(y);
   const Tensor n = !pre ? Tensor() : normed_out ? *normed_out : at::empty_like(y);
+  const Tensor st = stats ? fresh({static_cast<int64_t>(z.rows) * z.groups, 2}, F32, y) : Tensor();
   DL_CALL(dl_block_norm, ptr<int>(slot_idx), size_of("slots", slots), z.rows, z.D, z.groups, z.dt, ptr(y), ptr<float>(post), ptr(gate),
-          ptr<float>(scale), ptr(residual), ptr<float>(pre), static_cast<float>(eps), ptr(o), ptr(n), stream_of(y));
+          ptr<float>(scale), ptr(residual), ptr<float>(pre), static_cast<float>(eps), ptr(o), ptr(n), ptr<float>(st), stream_of(y));
   if (out) written(o);
   if (normed_out) written(n);
-  return {o, n};
+  return {o, n, st};
 }
 
 using SixTensors = std::tuple<Tensor, Tensor, Tensor, Tensor, Tensor, Tensor>;
 
 // In the order y, post, gate, scale, residual, pre; bit i of `need`: wanted.
-SixTensors norm_backward(const Tensor& y, const OptTensor& dout, const OptTensor& dnormed, const OptTensor& post, const OptTensor& gate,
+SixTensors norm_backward(const Tensor& y, const OptTensor& stats, const OptTensor& dout, const OptTensor& dnormed, const OptTensor& post, const OptTensor& gate,
                          const OptTensor& scale, const OptTensor& residual, const OptTensor& pre, int64_t groups, double eps, int64_t need) {
   const NormSizes z = norm_check(y, post, gate, scale, residual, pre, groups);
   TORCH_CHECK_VALUE(!dnormed || pre, "dnormed goes with pre_weight");
+  check("stats", stats, {static_cast<int64_t>(z.rows) * z.groups, 2}, F32, y.device());
+  TORCH_CHECK_VALUE(stats || !(post || pre), "stats is required");
   check("dout", dout, y.sizes(), y.scalar_type(), y.device());
   check("dnormed", dnormed, y.sizes(), y.scalar_type(), y.device());
   check_cuda("y", y);
@@ -295,7 +298,7 @@ SixTensors norm_backward(const Tensor& y, const OptTensor& dout, const OptTensor
     work = fresh({static_cast<int64_t>(bytes) + 1}, at::kByte, y);
   }
   DL_CALL(dl_block_norm_backward, z.rows, z.D, z.groups, z.dt, ptr(y), ptr<float>(post), ptr(gate), ptr<float>(scale), ptr(residual),
-          ptr<float>(pre), static_cast<float>(eps), ptr(dout), ptr(dnormed), ptr(dy), ptr(dgate), ptr(dres), ptr<float>(dpost),
+          ptr<float>(pre), static_cast<float>(eps), ptr<float>(stats), ptr(dout), ptr(dnormed), ptr(dy), ptr(dgate), ptr(dres), ptr<float>(dpost),
           ptr<float>(dscale), ptr<float>(dpre), ptr(work), stream_of(y));
   return {dy, dpost, dgate, dscale, dres, dpre};
 }
@@ -303,8 +306,8 @@ SixTensors norm_backward(const Tensor& y, const OptTensor& dout, const OptTensor
 struct BlockNorm : torch::autograd::Function<BlockNorm> {
   static variable_list forward(AutogradContext* ctx, const Tensor& y, const OptTensor& post, const OptTensor& gate, const OptTensor& scale,
                                const OptTensor& residual, const OptTensor& pre, int64_t groups, double eps) {
-    auto [out, normed] = norm_forward(y, post, gate, scale, residual, pre, groups, eps, std::nullopt, 0, std::nullopt, std::nullopt);
-    ctx->save_for_backward({y, opt(post), opt(gate), opt(scale), opt(residual), opt(pre)});
+    auto [out, normed, stats] = norm_run(y, post, gate, scale, residual, pre, groups, eps, std::nullopt, 0, std::nullopt, std::nullopt, post || pre);
+    ctx->save_for_backward({y, opt(post), opt(gate), opt(scale), opt(residual), opt(pre), stats});
     int64_t need = y.requires_grad();
     const OptTensor* const parts[] = {&post, &gate, &scale, &residual, &pre};
     for (int i = 0; i < 5; ++i)
@@ -320,7 +323,7 @@ struct BlockNorm : torch::autograd::Function<BlockNorm> {
     const auto s = ctx->get_saved_variables();
     const auto grad = [&](size_t i) { return i < g.size() && g[i].defined() ? OptTensor(g[i].contiguous()) : std::nullopt; };
     auto [dy, dpost, dgate, dscale, dres, dpre] =
-        norm_backward(s[0], grad(0), grad(1), opt(s[1]), opt(s[2]), opt(s[3]), opt(s[4]), opt(s[5]), ctx->saved_data["groups"].toInt(),
+        norm_backward(s[0], opt(s[6]), grad(0), grad(1), opt(s[1]), opt(s[2]), opt(s[3]), opt(s[4]), opt(s[5]), ctx->saved_data["groups"].toInt(),
                       ctx->saved_data["eps"].toDouble(), ctx->saved_data["need"].toInt());
     return once({dy, dpost, dgate, dscale, dres, dpre, Tensor(), Tensor()});
   }
@@ -335,7 +338,13 @@ std::tuple<Tensor, Tensor> block_norm(const Tensor& y, const OptTensor& post, co
     auto v = BlockNorm::apply(y, post, gate, scale, residual, pre, groups, eps);
     return {v[0], v.size() > 1 ? v[1] : Tensor()};
   }
-  return norm_forward(y, post, gate, scale, residual, pre, groups, eps, slot_idx, slots, out, normed_out);
+  auto [o, n, stats] = norm_run(y, post, gate, scale, residual, pre, groups, eps, slot_idx, slots, out, normed_out, false);
+  return {o, n};
+}
+
+std::tuple<Tensor, Tensor, Tensor> norm_forward(const Tensor& y, const OptTensor& post, const OptTensor& gate, const OptTensor& scale,
+                                                const OptTensor& residual, const OptTensor& pre, int64_t groups, double eps) {
+  return norm_run(y, post, gate, scale, residual, pre, groups, eps, std::nullopt, 0, std::nullopt, std::nullopt, true);
 }
 
 // -- paged key-value cache -------------------------------------------------------------
@@ -427,7 +436,10 @@ TORCH_LIBRARY(deltalog, m) {
   m.def("block_norm(Tensor y, Tensor? post_weight, Tensor? gate, Tensor? scale, Tensor? residual, Tensor? pre_weight, int groups, float eps, "
         "Tensor? slot_idx, int slots, Tensor? out, Tensor? normed_out) -> (Tensor, Tensor)",
         block_norm);
-  m.def("block_norm_backward(Tensor y, Tensor? dout, Tensor? dnormed, Tensor? post_weight, Tensor? gate, Tensor? scale, Tensor? residual, "
+  m.def("block_norm_forward(Tensor y, Tensor? post_weight, Tensor? gate, Tensor? scale, Tensor? residual, Tensor? pre_weight, int groups, "
+        "float eps) -> (Tensor, Tensor, Tensor)",
+        norm_forward);
+  m.def("block_norm_backward(Tensor y, Tensor? stats, Tensor? dout, Tensor? dnormed, Tensor? post_weight, Tensor? gate, Tensor? scale, Tensor? residual, "
         "Tensor? pre_weight, int groups, float eps, int need) -> (Tensor, Tensor, Tensor, Tensor, Tensor, Tensor)",
         norm_backward);
   m.def("paged_attention(Tensor q, Tensor k_pages, Tensor v_pages, Tensor block_table, Tensor lens, Tensor? k, Tensor? v, Tensor? slot_idx, "

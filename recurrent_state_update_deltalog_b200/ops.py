@@ -37,7 +37,7 @@ torch.ops.load_library(TORCH_LIB_PATH)
 _T = torch.ops.deltalog
 _scan, _scan_forward, _scan_backward = _T.gated_scan.default, _T.gated_scan_forward.default, _T.gated_scan_backward.default
 _scan_prefill, _scan_step = _T.gated_scan_prefill.default, _T.gated_scan_step.default
-_norm, _norm_backward = _T.block_norm.default, _T.block_norm_backward.default
+_norm, _norm_forward, _norm_backward = _T.block_norm.default, _T.block_norm_forward.default, _T.block_norm_backward.default
 _attention, _write = _T.paged_attention.default, _T.paged_write.default
 _STATUS = {name: code for code, name in N.STATUS.items()}
 
@@ -138,12 +138,19 @@ def block_norm(y, post_weight=None, gate=None, scale=None, residual=None, pre_we
     return pair[0] if pre_weight is None else pair
 
 
-def block_norm_backward(y, dout, dnormed=None, post_weight=None, gate=None, scale=None, residual=None, pre_weight=None,
-                        groups=1, eps=1e-6, need=(True,) * 6, stream=None):
-    """Gradients of :func:`block_norm` for dout and dnormed (each None: zeros), in the
-    order y, post_weight, gate, scale, residual, pre_weight; None for absent parts and
+def block_norm_forward(y, post_weight=None, gate=None, scale=None, residual=None, pre_weight=None, groups=1, eps=1e-6,
+                       stream=None):
+    """:func:`block_norm` without autograd: (out, normed, stats), normed None without a
+    pre_weight, stats being what :func:`block_norm_backward` needs."""
+    return _call(_norm_forward, y, stream, post_weight, gate, scale, residual, pre_weight, groups, eps)
+
+
+def block_norm_backward(y, stats, dout, dnormed=None, post_weight=None, gate=None, scale=None, residual=None,
+                        pre_weight=None, groups=1, eps=1e-6, need=(True,) * 6, stream=None):
+    """Gradients of :func:`block_norm_forward` for dout and dnormed (each None: zeros), in
+    the order y, post_weight, gate, scale, residual, pre_weight; None for absent parts and
     where ``need`` says False."""
-    return _call(_norm_backward, y, stream, dout, dnormed, post_weight, gate, scale, residual, pre_weight, groups, eps,
+    return _call(_norm_backward, y, stream, stats, dout, dnormed, post_weight, gate, scale, residual, pre_weight, groups, eps,
                  sum(1 << i for i, k in enumerate(need) if k))
 
 

@@ -217,12 +217,13 @@ def test_unaligned_views():
 
 def test_stream_and_captured_graphs():
     """Backward on another stream, and in two captured graphs with a workspace each, gives the eager bits."""
-    from recurrent_state_update_deltalog_b200 import block_norm_backward
+    from recurrent_state_update_deltalog_b200 import block_norm_backward, block_norm_forward
     t = {k: x.cuda() for k, x in make(600, 512, 1, torch.bfloat16, 14, ALL).items()}
 
     def back(**kw):
-        return block_norm_backward(t["y"], t["dout"], t["dnormed"], t["post_weight"], t["gate"], t["scale"], t["residual"],
-                                   t["pre_weight"], **kw)
+        parts = (t["post_weight"], t["gate"], t["scale"], t["residual"], t["pre_weight"])
+        out, normed, stats = block_norm_forward(t["y"], *parts, **kw)
+        return (out, normed, *block_norm_backward(t["y"], stats, t["dout"], t["dnormed"], *parts, **kw))
 
     want = [x.clone() for x in back()]
     side = torch.cuda.Stream()

@@ -101,7 +101,7 @@ def test_scan_python_refusals(lib):
 
 def norm_args(**over):
     a = dict(slot_idx=None, slots=0, rows=2, D=8, groups=1, dtype=1, y=P, post=None, gate=None, scale=None, residual=None,
-             pre=None, eps=1e-6, out=P, normed=None)
+             pre=None, eps=1e-6, out=P, normed=None, stats=None)
     a.update(over)
     return list(a.values()) + [None]
 
@@ -111,7 +111,7 @@ def norm_args(**over):
     (dict(D=8193), UNSUPPORTED), (dict(D=8200, groups=1), UNSUPPORTED), (dict(groups=2, scale=P), UNSUPPORTED),
     (dict(groups=2, pre=P, normed=P), UNSUPPORTED), (dict(eps=-1.0), ARG), (dict(eps=float("nan")), ARG), (dict(y=None), ARG),
     (dict(out=None), ARG), (dict(pre=P), ARG), (dict(normed=P), ARG), (dict(y=ODD), ARG), (dict(out=ODD), ARG),
-    (dict(post=ODD), ARG), (dict(slot_idx=P, slots=0), ARG), (dict(slot_idx=ODD, slots=2), ARG),
+    (dict(post=ODD), ARG), (dict(stats=ctypes.c_void_p(68)), ARG), (dict(slot_idx=P, slots=0), ARG), (dict(slot_idx=ODD, slots=2), ARG),
     (dict(rows=1 << 30, groups=4), UNSUPPORTED),
 ])
 def test_norm_refusals(lib, over, status):
@@ -120,12 +120,13 @@ def test_norm_refusals(lib, over, status):
 
 @pytest.mark.parametrize("over,status", [
     (dict(D=8193), UNSUPPORTED), (dict(y=None), ARG), (dict(dgate=P), ARG), (dict(dresidual=P), ARG), (dict(dpost=P), ARG),
-    (dict(dscale=P), ARG), (dict(dpre=P), ARG), (dict(dnormed=P), ARG), (dict(post=P, dpost=P), ARG), (dict(dy=ODD), ARG),
+    (dict(dscale=P), ARG), (dict(dpre=P), ARG), (dict(dnormed=P), ARG), (dict(post=P, dpost=P, stats=P), ARG), (dict(post=P), ARG), (dict(pre=P), ARG),
+    (dict(post=P, stats=ctypes.c_void_p(68)), ARG), (dict(dy=ODD), ARG),
     (dict(dout=ODD), ARG),
 ])
 def test_norm_backward_refusals(lib, over, status):
     a = dict(rows=2, D=8, groups=1, dtype=1, y=P, post=None, gate=None, scale=None, residual=None, pre=None, eps=1e-6,
-             dout=P, dnormed=None, dy=P, dgate=None, dresidual=None, dpost=None, dscale=None, dpre=None, work=None)
+             stats=None, dout=P, dnormed=None, dy=P, dgate=None, dresidual=None, dpost=None, dscale=None, dpre=None, work=None)
     a.update(over)
     assert lib.dl_block_norm_backward(*a.values(), None) == status
 
@@ -158,8 +159,10 @@ def test_norm_python_refusals(lib):
         (lambda: block_norm(y, w, out=y[:2]), "out"),
         (lambda: block_norm(y, w, slot_idx=idx[:2]), "slot_idx"),
         (lambda: block_norm(grad, w, out=y), "without gradients"),
-        (lambda: block_norm_backward(y, y, dnormed=y), "pre_weight"),
-        (lambda: block_norm_backward(y, y[:2]), "dout"),
+        (lambda: block_norm_backward(y, None, y, dnormed=y), "pre_weight"),
+        (lambda: block_norm_backward(y, None, y[:2]), "dout"),
+        (lambda: block_norm_backward(y, None, y, post_weight=w), "stats"),
+        (lambda: block_norm_backward(y, w, y, post_weight=w), "stats"),
     ]:
         with pytest.raises(ValueError, match=match):
             bad()
