@@ -90,8 +90,27 @@ cudaError_t run_ring(const NormArgs& a, const Shape& s, int ctas, bool back, cud
   return cudaGetLastError();
 }
 
+// Backward, wide rows of one piece a thread, from four rows a CTA on.
+template <typename T, bool GATE, bool PRE>
+cudaError_t run_pipe(const NormArgs& a, const Shape& s, int ctas, cudaStream_t st) {
+  const auto kern = dl::norm_backward_pipe_kernel<T, GATE, PRE>;
+  const int smem = 4 * (2 + GATE + 2 * PRE) * 16 * s.block();
+  if (smem > 40 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  kern<<<ctas, s.block(), smem, st>>>(a);
+  return cudaGetLastError();
+}
+
 template <typename T, int NV, bool NARROW>
 cudaError_t run_ring(const NormArgs& a, const Shape& s, int ctas, bool back, cudaStream_t st) {
+  if constexpr (NV == 1 && !NARROW) {
+    if (back && a.rows >= 4ll * ctas) {
+      if (a.gate) return a.pre ? run_pipe<T, true, true>(a, s, ctas, st) : run_pipe<T, true, false>(a, s, ctas, st);
+      return a.pre ? run_pipe<T, false, true>(a, s, ctas, st) : run_pipe<T, false, false>(a, s, ctas, st);
+    }
+  }
   if (a.gate) return a.pre ? run_ring<T, NV, NARROW, true, true>(a, s, ctas, back, st) : run_ring<T, NV, NARROW, true, false>(a, s, ctas, back, st);
   return a.pre ? run_ring<T, NV, NARROW, false, true>(a, s, ctas, back, st) : run_ring<T, NV, NARROW, false, false>(a, s, ctas, back, st);
 }

@@ -369,18 +369,18 @@ __global__ void __launch_bounds__(NARROW ? kNormNarrow : 512, NARROW ? 2 : 1) no
     ring.issue(s, row + S * step, row + S * step < a.rows, lane, a.tpr, a.n);
     const float r1 = ahead.x, r2 = ahead.y;
     ahead = stats_of(row + step);
-    float2 t[NV][P], u[NV][P], slope[NV][P], D[NV][P];  // post yn, act t, silu'(gate), gradient of out
+    float2 act[NV][P], slope[NV][P], u[NV][P], D[NV][P];  // silu(gate), its slope, act post yn, gradient of out
     float2 S1 = both(0.f), S2 = both(0.f), S3 = both(0.f), S4 = both(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int j = 0; j < P; ++j) {
-        t[i][j] = mul2(mul2(y[i].pair(j), both(r1)), post.v[i][j]);
-        u[i][j] = t[i][j];
+        u[i][j] = mul2(mul2(y[i].pair(j), both(r1)), post.v[i][j]);
         if constexpr (GATE) {
-          const float2 f = g[i].pair(j), sg = make_float2(sigmoid(f.x), sigmoid(f.y)), act = mul2(f, sg);
-          slope[i][j] = fma2(act, fma2(sg, both(-1.f), both(1.f)), sg);
-          u[i][j] = mul2(act, u[i][j]);
+          const float2 f = g[i].pair(j), sg = make_float2(sigmoid(f.x), sigmoid(f.y));
+          act[i][j] = mul2(f, sg);
+          slope[i][j] = fma2(act[i][j], fma2(sg, both(-1.f), both(1.f)), sg);
+          u[i][j] = mul2(act[i][j], u[i][j]);
         }
         const float2 m = mul2(scale.v[i][j], u[i][j]), dout = po[i].pair(j);
         S2 = fma2(m, dout, S2);
@@ -425,9 +425,8 @@ __global__ void __launch_bounds__(NARROW ? kNormNarrow : 512, NARROW ? 2 : 1) no
         const float2 Ds = mul2(D[i][j], scale.v[i][j]), yn = mul2(y[i].pair(j), both(r1));
         float2 e = Ds;
         if constexpr (GATE) {
-          const float2 f = g[i].pair(j);
-          wg.set(j, mul2(mul2(Ds, t[i][j]), slope[i][j]));
-          e = mul2(e, mul2(f, make_float2(sigmoid(f.x), sigmoid(f.y))));
+          wg.set(j, mul2(mul2(Ds, mul2(yn, post.v[i][j])), slope[i][j]));
+          e = mul2(e, act[i][j]);
         }
         sums[0][i][j] = fma2(e, yn, sums[0][i][j]);
         wy.set(j, fma2(y[i].pair(j), both(-ky), mul2(mul2(e, post.v[i][j]), both(r1))));
@@ -452,6 +451,196 @@ __global__ void __launch_bounds__(NARROW ? kNormNarrow : 512, NARROW ? 2 : 1) no
         flat[p][i][2 * j + 1] = sums[p][i][j].y;
       }
   put_sums<NV, V, NARROW>(a, flat, reinterpret_cast<float*>(ring_places), lane, sub, per);
+}
+
+// -- many wide rows, backward: rows in a pipeline ------------------------------------
+//
+// A row's sums have to meet across the CTA before its gradients can be formed.  With
+// one row at a time every warp waits there.  So row i + 1's sums are formed before
+// row i's gradients, both from the ring: what its threads send each other travels
+// meanwhile, and one barrier a row is enough.  The second conversion and sigmoid
+// cost less than the wait: 16384 x 4096 bf16 267 us one row at a time, 248 us so (the
+// same traffic without the arithmetic: 175 us).  The forward pass, interleaved over
+// three rows in the same way, went from 132 to 169 us: it stays as it is.
+
+// Sums of K values over a CTA's threads in two halves: send() leaves a warp's in
+// shared memory, get() after the barrier adds them up.
+template <int K>
+struct RowExchange {
+  float (*sm)[32][4];
+  __device__ __forceinline__ void send(int turn, const float (&v)[K]) const {
+    const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
+    if constexpr (K == 4) {
+      const bool up = lane & 16, odd = lane & 8;
+      float a = up ? v[2] : v[0], b = up ? v[3] : v[1];
+      a += __shfl_xor_sync(~0u, up ? v[0] : v[2], 16);
+      b += __shfl_xor_sync(~0u, up ? v[1] : v[3], 16);
+      float c = odd ? b : a;
+      c += __shfl_xor_sync(~0u, odd ? a : b, 8);
+      c += __shfl_xor_sync(~0u, c, 4);
+      c += __shfl_xor_sync(~0u, c, 2);
+      c += __shfl_xor_sync(~0u, c, 1);
+      if ((lane & 7) == 0) sm[turn][w][lane / 8] = c;
+    } else {
+      float c = v[0];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(~0u, c, o);
+      if (lane == 0) sm[turn][w][0] = c;
+    }
+  }
+  __device__ __forceinline__ void get(int turn, int warps, float (&v)[K]) const {
+    const int lane = threadIdx.x % 32;
+    float c = 0.f;
+    for (int w = lane / K; w < warps; w += 32 / K) c += sm[turn][w][lane % K];
+#pragma unroll
+    for (int o = K; o < 32; o <<= 1) c += __shfl_xor_sync(~0u, c, o);
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = K == 1 ? c : __shfl_sync(~0u, c, k);
+  }
+};
+
+// 16 bytes a thread and tensor.
+template <typename T, bool GATE, bool PRE>
+__global__ void __launch_bounds__(512, 1) norm_backward_pipe_kernel(NormArgs a) {
+  constexpr int V = 16 / sizeof(T), P = V / 2, K = 2 + GATE + 2 * PRE, S = 4, KS = PRE ? 4 : 1;
+  extern __shared__ __align__(16) uint4 ring_places[];
+  __shared__ float sm[2][32][4];
+  const int lane = threadIdx.x, c = lane * V, warps = a.tpr / 32;
+  const float inv = 1.f / static_cast<float>(a.n);
+  NormRing<T, 1, K, S> ring{ring_places + threadIdx.x, static_cast<int>(blockDim.x)};
+  ring.set(0, a.y, a.y);
+  ring.set(1, a.dout, a.y);
+  if constexpr (GATE) ring.set(2, a.gate, a.y);
+  if constexpr (PRE) {
+    ring.set(2 + GATE, a.residual, a.y);
+    ring.set(3 + GATE, a.dnormed, a.y);
+  }
+  const RowExchange<KS> ex{sm};
+  const long long step = gridDim.x;
+  const int rows = static_cast<int>((a.rows - blockIdx.x + step - 1) / step);  // of this CTA
+  auto row_of = [&](int i) { return blockIdx.x + i * step; };
+  auto stats_of = [&](int i) { return a.stats && i < rows ? __ldg(reinterpret_cast<const float2*>(a.stats) + row_of(i)) : both(1.f); };
+#pragma unroll
+  for (int s = 0; s < S - 1; ++s) ring.issue(s, row_of(s), s < rows, lane, a.tpr, a.n);
+  Weights<1, V> post, scale, pre;
+  post.load(a.post, lane, a.tpr, a.n);
+  scale.load(a.scale, lane, a.tpr, a.n);
+  if constexpr (PRE) pre.load(a.pre, lane, a.tpr, a.n);
+  float2 sums[3][P];
+#pragma unroll
+  for (int j = 0; j < P; ++j) sums[0][j] = sums[1][j] = sums[2][j] = both(0.f);
+  float2 r = both(1.f), next = stats_of(0), ahead;  // r1, r2 of rows i, i + 1, i + 2
+  float k = 0.f, ky = 0.f;                          // of row i: mean(d on); r1^2 mean(e yn), as dy = r1 e - y ky
+  for (int i = -1; i < rows; ++i) {
+    ahead = stats_of(i + 2);
+    copy_wait<S - 2>();  // row i + 1 is here
+    float v[KS];
+#pragma unroll
+    for (int q = 0; q < KS; ++q) v[q] = 0.f;
+    if (i + 1 < rows) {
+      const int s = (i + 1) & (S - 1);
+      const Piece<T> y = ring.get(s, 0, 0), po = ring.get(s, 1, 0);
+      Piece<T> g, x, pn;
+      if constexpr (GATE) g = ring.get(s, 2, 0);
+      if constexpr (PRE) {
+        x = ring.get(s, 2 + GATE, 0);
+        pn = ring.get(s, 3 + GATE, 0);
+      }
+      float2 S1 = both(0.f), S2 = both(0.f), S3 = both(0.f), S4 = both(0.f);
+#pragma unroll
+      for (int j = 0; j < P; ++j) {
+        float2 m = mul2(mul2(mul2(y.pair(j), both(next.x)), post.v[0][j]), scale.v[0][j]);
+        if constexpr (GATE) {
+          const float2 f = g.pair(j);
+          m = mul2(mul2(f, make_float2(sigmoid(f.x), sigmoid(f.y))), m);
+        }
+        S2 = fma2(m, po.pair(j), S2);
+        if constexpr (PRE) {
+          const float2 out = __fadd2_rn(m, x.pair(j)), d = mul2(pn.pair(j), pre.v[0][j]);
+          S1 = fma2(d, out, S1);
+          S3 = fma2(m, d, S3);
+          S4 = fma2(m, out, S4);
+        }
+      }
+      if constexpr (PRE) {
+        v[0] = S1.x + S1.y;
+        v[1] = S2.x + S2.y;
+        v[2] = S3.x + S3.y;
+        v[3] = S4.x + S4.y;
+      } else {
+        v[0] = S2.x + S2.y;
+      }
+    }
+    const int turn = i & 1;
+    ex.send(turn, v);
+    if (i >= 0) {
+      const int s = i & (S - 1);
+      const Piece<T> y = ring.get(s, 0, 0), po = ring.get(s, 1, 0);
+      Piece<T> g, x, pn, wx, wg, wy;
+      if constexpr (GATE) g = ring.get(s, 2, 0);
+      if constexpr (PRE) {
+        x = ring.get(s, 2 + GATE, 0);
+        pn = ring.get(s, 3 + GATE, 0);
+      }
+#pragma unroll
+      for (int j = 0; j < P; ++j) {
+        const float2 yn = mul2(y.pair(j), both(r.x)), t = mul2(yn, post.v[0][j]);
+        float2 act, sg, u = t;
+        if constexpr (GATE) {
+          const float2 f = g.pair(j);
+          sg = make_float2(sigmoid(f.x), sigmoid(f.y));
+          act = mul2(f, sg);
+          u = mul2(act, t);
+        }
+        float2 D = po.pair(j);  // gradient of out
+        if constexpr (PRE) {
+          const float2 on = mul2(fma2(scale.v[0][j], u, x.pair(j)), both(r.y)), dn = pn.pair(j);
+          sums[2][j] = fma2(dn, on, sums[2][j]);
+          D = fma2(both(r.y), fma2(on, both(-k), mul2(dn, pre.v[0][j])), D);
+        }
+        wx.set(j, D);
+        sums[1][j] = fma2(D, u, sums[1][j]);
+        float2 e = mul2(D, scale.v[0][j]);
+        if constexpr (GATE) {
+          wg.set(j, mul2(mul2(e, t), fma2(act, fma2(sg, both(-1.f), both(1.f)), sg)));
+          e = mul2(e, act);
+        }
+        sums[0][j] = fma2(e, yn, sums[0][j]);
+        wy.set(j, fma2(y.pair(j), both(-ky), mul2(mul2(e, post.v[0][j]), both(r.x))));
+      }
+      const long long at = row_of(i) * a.n + c;
+      if (c < a.n) {
+        if (a.dresidual) wx.store(static_cast<T*>(a.dresidual) + at);
+        if constexpr (GATE) {
+          if (a.dgate) wg.store(static_cast<T*>(a.dgate) + at);
+        }
+        if (a.dy) wy.store(static_cast<T*>(a.dy) + at);
+      }
+    }
+    ring.issue((i + S) & (S - 1), row_of(i + S), i + S < rows, lane, a.tpr, a.n);  // row i's places
+    __syncthreads();
+    ex.get(turn, warps, v);
+    r = next;
+    next = ahead;
+    if constexpr (PRE) {
+      k = v[0] * inv * r.y;
+      ky = fmaf(r.y, fmaf(-k * r.y, v[3], v[2]), v[1]);
+    } else {
+      ky = v[0];
+    }
+    ky = a.post ? ky * inv * r.x * r.x : 0.f;
+  }
+  copy_wait<0>();
+  if (!a.partial) return;
+  float flat[3][1][V];
+#pragma unroll
+  for (int p = 0; p < 3; ++p)
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+      flat[p][0][2 * j] = sums[p][j].x;
+      flat[p][0][2 * j + 1] = sums[p][j].y;
+    }
+  put_sums<1, V, false>(a, flat, nullptr, lane, 0, 1);
 }
 
 // -- rows on any address -------------------------------------------------------------

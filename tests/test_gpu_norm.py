@@ -142,6 +142,14 @@ def test_parts(parts, D, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("parts", PARTS, ids="-".join)
+@pytest.mark.parametrize("rows,D", [(1500, 2048), (4800, 512), (4737, 520)])
+def test_many_rows(rows, D, parts, dtype):
+    """Enough rows that each CTA takes several, the last ones fewer."""
+    compare(make(rows, D, 1, dtype, 6, parts), 1, 1e-6, dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("rows,H,d", [(1, 1, 64), (5, 3, 64), (700, 4, 128), (3, 7, 33), (2, 5, 300), (1500, 2, 16)])
 @pytest.mark.parametrize("parts", [("post_weight", "gate"), ("post_weight", "residual")], ids="-".join)
 def test_groups(rows, H, d, parts, dtype):
