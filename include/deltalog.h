@@ -499,8 +499,8 @@ int dl_block_norm_backward(int rows, int D, int groups, int in_dtype, const void
  *   q, out      typed [rows][Hq][d] (out may be q);
  *   k, v        typed [rows][Hkv][d], the new token's, stored at position
  *               lens[s] - 1 and used from here; both NULL: already stored.
- * Hq a multiple of Hkv; d in {64, 128}; page_size a power of two; pointers of
- * typed tensors 16-byte aligned.  The split over the length follows max_pages
+ * Hq a multiple of Hkv; d in {64, 128}; page_size a power of two; num_pages *
+ * Hkv * page_size < 2^31; pointers of typed tensors 16-byte aligned.  The split over the length follows max_pages
  * (or the window), so a table no wider than needed is fastest.  Scores and
  * sums are fp32; with bf16 the weights enter their product with v as bf16.
  *   workspace   16-byte aligned buffer of dl_paged_attention_workspace bytes

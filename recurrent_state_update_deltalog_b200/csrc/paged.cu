@@ -22,6 +22,8 @@ int check(const int* slot_idx, int slots, int rows, int Hkv, int d, int dtype, i
   if (rows > 65535) return unsupported("at most 65535 rows (grid y)");
   if (page_size < 1 || page_size > (1 << 20) || (page_size & (page_size - 1)))
     return unsupported("page_size not a power of two in [1, 2^20]");
+  if (num_pages > 0 && static_cast<double>(num_pages) * Hkv * page_size >= 2147483648.0)
+    return unsupported("2^31 or more rows of keys");
   if (num_pages > INT_MAX || Hkv > 65535) return unsupported("page ids are 32-bit, at most 65535 key-value heads");
   if (static_cast<long long>(max_pages) * page_size > (1 << 30)) return unsupported("more than 2^30 positions a slot");
   if (rows == 0) return DL_OK;
@@ -57,7 +59,7 @@ struct Split {
 // as long as every warp finds two tiles in the longest row the table allows.
 // The even form if a warp would then have more than eight.  B200, bf16, d = 128,
 // 8 key-value heads of 4, clusters / even: 8 rows of 1024 tokens (4 tiles a
-// warp) 13.5 / 16.8 us; 32 ragged rows of up to 4096 tokens (64) 65 / 47 us.
+// warp) 13.5 / 16.8 us; 32 ragged rows of up to 4096 tokens (64) 65 / 54 us.
 Split split_of(int rows, int G, int Hkv, int dtype, long long longest) {
   Split s{};
   s.heads = dtype == DL_BF16 ? (G > 8 ? 16 : 8) : G > 2 ? 4 : G;
@@ -68,7 +70,7 @@ Split split_of(int rows, int G, int Hkv, int dtype, long long longest) {
   while (s.ctas < 8 && 2 * units * s.ctas < 3 * kSms && 2 * s.ctas * 4 * 2 <= tiles) s.ctas *= 2;
   if (tiles > 8 * 4 * s.ctas && rows <= dl::kPagedRows) {
     s.even = true;
-    const long long runs = (units * tiles + dl::kPagedRun - 1) / dl::kPagedRun;  // most that have work
+    const long long runs = (units * (tiles + dl::kPagedStart) + dl::kPagedRun - 1) / dl::kPagedRun;  // most that have work
     const int resident = kSms * (s.heads > 8 ? 2 : 3);
     s.ctas = static_cast<int>(runs < resident ? runs : resident);
   }

@@ -50,7 +50,7 @@ struct PagedArgs {
   int head_blocks;        // CTAs' head groups a key-value head
   // shared evenly: each CTA's triples of the (row, head) it found begun [2i] and
   // of the one it left unfinished [2i + 1], [2 * CTAs][HT][d + 2]; and the plan,
-  // [rows + 1] tiles before each row and [1] tiles of a CTA
+  // [rows + 1] cost before each row and [1] cost of a CTA, in tiles
   float* parts;
   long long* plan;
   int rows;
@@ -96,8 +96,14 @@ __device__ __forceinline__ float load_remote(uint32_t addr) {
   return x;
 }
 
-// 2^x, and 0 for -inf; the first operand may be -inf like the second.
-__device__ __forceinline__ float exp2_diff(float x, float m) { return m == -INFINITY ? 0.f : exp2f(x - m); }
+// 2^x to 2^-22 of itself.
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// 2^(x - m), where both may be -inf: 0.
+__device__ __forceinline__ float exp2_diff(float x, float m) { return exp2_fast(x - (m == -INFINITY ? 0.f : m)); }
 
 // Page of position `pos` of a slot's table row, or -1 (reported).
 __device__ __forceinline__ long long page_of(const PagedArgs& a, const int* table, int pos) {
@@ -126,6 +132,7 @@ __device__ __forceinline__ bool paged_row(const PagedArgs& a, int r, bool tell, 
 constexpr int kTile = 16;        // tokens of a tile
 constexpr int kPagedRows = 1024; // rows of a launch that shares its tiles evenly
 constexpr int kPagedRun = 32;    // fewest tiles of its CTAs: 8 a warp
+constexpr int kPagedStart = 16;  // what starting a unit costs, in tiles
 
 // A piece of one (row, key-value head, head group): tiles [from, to) of the row.
 struct PagedPiece {
@@ -133,7 +140,12 @@ struct PagedPiece {
   bool begun, unfinished;  // tiles of the unit before `from`, behind `to`
 };
 
-// The even sharing: this CTA's run of the list of all tiles.
+// The even sharing: this CTA's run of the list of all tiles.  A unit weighs
+// kPagedStart tiles more than it has, for the latencies of its first loads and its
+// join; those come first in the list, and tile t of the unit stands at kPagedStart
+// + t.  With 0 / 4 / 8 / 16 / 32 tiles: 128 rows of 64 to 1024 tokens, 8 heads of
+// 64, 74 / 59 / 48 / 43 / 44 us; 64 rows of 512 to 8192 tokens, 4 heads of 128,
+// 102 / 100 / 94 / 93 / 95 us; equal rows 169 / 169 / 169 / 171 / 171 us.
 struct PagedRun {
   long long at, end;  // list positions still to do
   int r;              // row of `at`
@@ -145,7 +157,7 @@ struct PagedRun {
     for (int i = threadIdx.x; i < a.rows; i += threads) {
       int slot, first, len;
       const bool there = paged_row(a, i, blockIdx.x == 0, &slot, &first, &len) && len > 0;
-      cum[i + 1] = there ? static_cast<long long>((len + kTile - 1) / kTile - first / kTile) * units : 0;
+      cum[i + 1] = there ? static_cast<long long>((len + kTile - 1) / kTile - first / kTile + kPagedStart) * units : 0;
     }
     if (threadIdx.x == 0) cum[0] = 0;
     __syncthreads();
@@ -182,25 +194,29 @@ struct PagedRun {
   }
 
   __device__ __forceinline__ bool next(const PagedArgs& a, PagedPiece* p) {
-    if (at >= end) return false;
-    while (before[r + 1] <= at) ++r;  // rows without tiles
-    p->r = r;
-    paged_row(a, r, false, &p->slot, &p->first, &p->len);
-    const int units = a.Hkv * a.head_blocks, tile0 = p->first / kTile;
-    const int tiles = static_cast<int>((before[r + 1] - before[r]) / units);
-    const long long in = at - before[r];  // below 2^31 tiles a row and 65535 heads: often short
-    const int unit = in >> 32 ? static_cast<int>(in / tiles) : static_cast<int>(static_cast<unsigned>(in) / tiles);
-    const int from = static_cast<int>(in - static_cast<long long>(unit) * tiles);
-    const long long left = end - at;
-    const int n = left < tiles - from ? static_cast<int>(left) : tiles - from;
-    p->kvh = unit / a.head_blocks;
-    p->hb = unit % a.head_blocks;
-    p->from = tile0 + from;
-    p->to = p->from + n;
-    p->begun = from > 0;
-    p->unfinished = from + n < tiles;
-    at += n;
-    return true;
+    while (at < end) {
+      while (before[r + 1] <= at) ++r;  // rows without tiles
+      const int units = a.Hkv * a.head_blocks;
+      const int cost = static_cast<int>((before[r + 1] - before[r]) / units), tiles = cost - kPagedStart;
+      const long long in = at - before[r];  // often short: a 64-bit division costs ten 32-bit ones
+      const int unit = in >> 32 ? static_cast<int>(in / cost) : static_cast<int>(static_cast<unsigned>(in) / cost);
+      const int from = static_cast<int>(in - static_cast<long long>(unit) * cost) - kPagedStart;
+      const long long left = end - at;
+      const int n = left < tiles - from ? static_cast<int>(left) : tiles - from;
+      at += n;
+      if (from + n <= 0) continue;  // no tile of the unit stands in this run
+      paged_row(a, r, false, &p->slot, &p->first, &p->len);
+      const int tile0 = p->first / kTile;
+      p->r = r;
+      p->kvh = unit / a.head_blocks;
+      p->hb = unit % a.head_blocks;
+      p->from = tile0 + (from > 0 ? from : 0);
+      p->to = tile0 + from + n;
+      p->begun = from > 0;
+      p->unfinished = from + n < tiles;
+      return true;
+    }
+    return false;
   }
 };
 
@@ -288,9 +304,9 @@ __global__ void __launch_bounds__(GR * D) paged_join_kernel(PagedArgs a) {
     return;
   }
   const int units = a.Hkv * a.head_blocks;
-  const long long begin = a.plan[r], tiles = (a.plan[r + 1] - begin) / units, run = a.plan[a.rows + 1];
-  const long long g0 = begin + (kvh * a.head_blocks + hb) * tiles;
-  const long long c0 = g0 / run, c1 = (g0 + tiles - 1) / run;  // the CTAs that share it
+  const long long begin = a.plan[r], cost = (a.plan[r + 1] - begin) / units, run = a.plan[a.rows + 1];
+  const long long g0 = begin + (kvh * a.head_blocks + hb) * cost;
+  const long long c0 = (g0 + kPagedStart) / run, c1 = (g0 + cost - 1) / run;  // the CTAs with its first and last tile
   if (c0 == c1) return;                                        // one: it is written
   // CTA c0 left it unfinished [2 c0 + 1], the others found it begun [2 c]
   auto triple = [&](long long c) { return a.parts + ((2 * c + (c == c0)) * HT + h) * (D + 2); };
@@ -398,64 +414,76 @@ __global__ void __launch_bounds__(W * 32, NT == 1 ? 3 : 2) paged_bf16_kernel(Pag
     const int mask = (1 << a.page_shift) - 1;
     const int stop = len < tiles * kTile ? len : tiles * kTile;               // positions of the piece
     const int old = a.k_new && stop == len ? len - 1 : stop;                  // those in the pages
-    // Page of a tile that lies whole in the old positions of one page; else -1:
-    // its rows are looked up one by one.
-    auto page_ahead = [&](int tile) {
-      if (tile * kTile < first || tile * kTile + 16 > old || a.page_shift < 4) return -1;
-      const int p = __ldg(table + (tile * kTile >> a.page_shift));
-      return p < a.pages ? p : -1;
+    // Pages of a tile's two halves of 8 positions, each of which lies in one page
+    // if pages hold 8 at least; -1: pages are smaller, or the half lies behind
+    // the piece.
+    auto page_ahead = [&](int tile, int (&page)[2]) {
+      const int pos = tile * kTile;
+      page[0] = page[1] = -1;
+      if (a.page_shift < 3 || pos >= stop) return;
+      page[0] = page[1] = __ldg(table + (pos >> a.page_shift));
+      if (a.page_shift == 3) page[1] = pos + 8 < stop ? __ldg(table + ((pos + 8) >> 3)) : -1;
     };
-    auto tile_at = [&](int page, int tile) {
-      return (((static_cast<long long>(page) * a.Hkv + kvh) << a.page_shift) + (tile * kTile & mask)) * D;
+    // Row of a position in the pages: the interface keeps rows below 2^31.
+    auto row_of = [&](int page, int pos) { return static_cast<uint32_t>(((page * a.Hkv + kvh) << a.page_shift) + (pos & mask)); };
+    auto known = [&](int page) { return static_cast<unsigned>(page) < static_cast<unsigned long long>(a.pages); };
+    // Whether a tile lies whole in the old positions of known pages.
+    auto whole = [&](int tile, const int (&page)[2]) {
+      return tile * kTile >= first && tile * kTile + kTile <= old && known(page[0]) && known(page[1]);
     };
-    // Element index of position `pos` in the pages, -1: not there, -2: the new token.
-    auto row_at = [&](int pos) -> long long {
-      if (pos < first || pos >= stop) return -1;
-      if (pos >= old) return -2;
-      const long long page = page_of(a, table, pos);
-      return page < 0 ? -1 : (((page * a.Hkv + kvh) << a.page_shift) + (pos & mask)) * D;
+    // Otherwise its rows are taken one by one: the row of `pos`, or null.
+    auto row_at = [&](int pos, int page, const bf16* pages, const void* fresh) -> const bf16* {
+      if (pos < first || pos >= stop) return nullptr;
+      if (pos >= old) return static_cast<const bf16*>(fresh) + new_at;
+      if (!known(page)) page = static_cast<int>(page_of(a, table, pos));
+      return page < 0 ? nullptr : pages + static_cast<size_t>(row_of(page, pos)) * D;
     };
+
     uint4 kf[TT][2][KB], vf[TT][4][VB];
     unsigned there = 0;  // bit 2x + s: score row s of this lane in tile x
-    auto load_keys = [&](int tile, const int (&page)[TT]) {
+    auto load_keys = [&](int tile, const int (&page)[TT][2]) {
       there = 0;
 #pragma unroll
       for (int x = 0; x < TT; ++x) {
-        if (page[x] >= 0) {
-          const bf16* const p = kp + tile_at(page[x], tile + x) + g * D + j * 8;
+        const int pos = (tile + x) * kTile;
+        if (whole(tile + x, page[x])) {
           there |= 3u << (2 * x);
 #pragma unroll
-          for (int s = 0; s < 2; ++s)
+          for (int s = 0; s < 2; ++s) {
+            const bf16* const p = kp + static_cast<size_t>(row_of(page[x][s], pos + s * 8)) * D + g * D + j * 8;
 #pragma unroll
-            for (int b = 0; b < KB; ++b) kf[x][s][b] = ld16(p + s * 8 * D + b * 32);
+            for (int b = 0; b < KB; ++b) kf[x][s][b] = ld16(p + b * 32);
+          }
         } else {
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
-            const long long at = row_at((tile + x) * kTile + g + s * 8);
-            const bf16* const p = at == -2 ? static_cast<const bf16*>(a.k_new) + new_at : kp + at;
-            if (at != -1) there |= 1u << (2 * x + s);
+            const bf16* const p = row_at(pos + s * 8 + g, page[x][s], kp, a.k_new);
+            if (p) there |= 1u << (2 * x + s);
 #pragma unroll
-            for (int b = 0; b < KB; ++b) kf[x][s][b] = at != -1 ? ld16(p + b * 32 + j * 8) : make_uint4(0, 0, 0, 0);
+            for (int b = 0; b < KB; ++b) kf[x][s][b] = p ? ld16(p + b * 32 + j * 8) : make_uint4(0, 0, 0, 0);
           }
         }
       }
     };
-    auto load_values = [&](int tile, const int (&page)[TT]) {
+    auto load_values = [&](int tile, const int (&page)[TT][2]) {
 #pragma unroll
       for (int x = 0; x < TT; ++x) {
-        if (page[x] >= 0) {
-          const bf16* const p = vp + tile_at(page[x], tile + x) + 2 * j * D + g * 8;
+        const int pos = (tile + x) * kTile;
+        if (whole(tile + x, page[x])) {
 #pragma unroll
-          for (int s = 0; s < 4; ++s)
+          for (int s = 0; s < 2; ++s) {
+            const bf16* const p = vp + static_cast<size_t>(row_of(page[x][s], pos + s * 8)) * D + 2 * j * D + g * 8;
 #pragma unroll
-            for (int b = 0; b < VB; ++b) vf[x][s][b] = ld16(p + ((s & 1) + (s >> 1) * 8) * D + b * 64);
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int b = 0; b < VB; ++b) vf[x][2 * s + i][b] = ld16(p + i * D + b * 64);
+          }
         } else {
 #pragma unroll
           for (int s = 0; s < 4; ++s) {
-            const long long at = row_at((tile + x) * kTile + 2 * j + (s & 1) + (s >> 1) * 8);
-            const bf16* const p = at == -2 ? static_cast<const bf16*>(a.v_new) + new_at : vp + at;
+            const bf16* const p = row_at(pos + (s >> 1) * 8 + 2 * j + (s & 1), page[x][s >> 1], vp, a.v_new);
 #pragma unroll
-            for (int b = 0; b < VB; ++b) vf[x][s][b] = at != -1 ? ld16(p + b * 64 + g * 8) : make_uint4(0, 0, 0, 0);
+            for (int b = 0; b < VB; ++b) vf[x][s][b] = p ? ld16(p + b * 64 + g * 8) : make_uint4(0, 0, 0, 0);
           }
         }
       }
@@ -463,11 +491,11 @@ __global__ void __launch_bounds__(W * 32, NT == 1 ? 3 : 2) paged_bf16_kernel(Pag
 
     const int step = N * W * TT;
     int tile = p.from + (rank * W + warp) * TT;
-    int page[TT], ahead[TT];
+    int page[TT][2], ahead[TT][2];
 #pragma unroll
     for (int x = 0; x < TT; ++x) {
-      page[x] = page_ahead(tile + x);
-      ahead[x] = page_ahead(tile + step + x);
+      page_ahead(tile + x, page[x]);
+      page_ahead(tile + step + x, ahead[x]);
     }
     if (tile < tiles) {
       load_keys(tile, page);
@@ -489,8 +517,9 @@ __global__ void __launch_bounds__(W * 32, NT == 1 ? 3 : 2) paged_bf16_kernel(Pag
       const unsigned here = there;
 #pragma unroll
       for (int x = 0; x < TT; ++x) {
-        page[x] = ahead[x];
-        ahead[x] = page_ahead(tile + 2 * step + x);
+        page[x][0] = ahead[x][0];
+        page[x][1] = ahead[x][1];
+        page_ahead(tile + 2 * step + x, ahead[x]);
       }
       const bool more = tile + step < tiles;
       if (more) load_keys(tile + step, page);
@@ -510,22 +539,28 @@ __global__ void __launch_bounds__(W * 32, NT == 1 ? 3 : 2) paged_bf16_kernel(Pag
           top[c] = fmaxf(top[c], __shfl_xor_sync(~0u, top[c], 4));
           top[c] = fmaxf(top[c], __shfl_xor_sync(~0u, top[c], 8));
           top[c] = fmaxf(top[c], __shfl_xor_sync(~0u, top[c], 16));
-          const float f = exp2_diff(m[t][c], top[c]);
-          m[t][c] = top[c];
-          l[t][c] *= f;
-#pragma unroll
-          for (int b = 0; b < VB; ++b)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              o[t][b][i][c] *= f;
-              o[t][b][i][c + 2] *= f;
-            }
         }
+        if (__any_sync(~0u, top[0] != m[t][0] || top[1] != m[t][1])) {  // a new maximum: rare after the first tiles
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float f = exp2_diff(m[t][c], top[c]);
+            m[t][c] = top[c];
+            l[t][c] *= f;
+#pragma unroll
+            for (int b = 0; b < VB; ++b)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                o[t][b][i][c] *= f;
+                o[t][b][i][c + 2] *= f;
+              }
+          }
+        }
+        const float low[2] = {m[t][0] == -INFINITY ? 0.f : m[t][0], m[t][1] == -INFINITY ? 0.f : m[t][1]};
 #pragma unroll
         for (int x = 0; x < TT; ++x) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            s[t][x][c] = exp2_diff(s[t][x][c], m[t][c & 1]);
+            s[t][x][c] = exp2_fast(s[t][x][c] - low[c & 1]);
             l[t][c & 1] += s[t][x][c];
           }
           w[t][x][0] = transpose8x8(pack_bf16(s[t][x][0], s[t][x][1]));
@@ -690,7 +725,7 @@ __global__ void __launch_bounds__(256) paged_write_kernel(PagedArgs a, int row_u
   const bool tell = blockIdx.x == 0 && threadIdx.x == 0;
   const int slot = row_slot(a.slot_idx, a.slots, r, a.err, tell);
   if (slot < 0) return;
-  const int s = __ldg(a.cu + r), e = __ldg(a.cu + r + 1), start = a.starts ? __ldg(a.starts + slot) : 0;
+  const int s = __ldg(a.cu + r), e = __ldg(a.cu + r + 1), start = kPagedStarts ? __ldg(kPagedStarts + slot) : 0;
   if (s < 0 || e < s || e > a.total || start < 0 ||
       static_cast<long long>(start) + e - s > (static_cast<long long>(a.max_pages) << a.page_shift)) {
     if (tell) raise_error(a.err, DL_DEVERR_SEQLEN);

@@ -178,7 +178,7 @@ def paged_args(**over):
 @pytest.mark.parametrize("over,status", [
     (dict(dtype=2), ARG), (dict(d=96), UNSUPPORTED), (dict(d=256), UNSUPPORTED), (dict(rows=-1), ARG), (dict(Hkv=0), ARG),
     (dict(Hq=5), ARG), (dict(Hq=0), ARG), (dict(page=0), UNSUPPORTED), (dict(page=12), UNSUPPORTED),
-    (dict(page=1 << 21), UNSUPPORTED), (dict(pages=-1), ARG), (dict(pages=1 << 31), UNSUPPORTED), (dict(max_pages=-1), ARG),
+    (dict(page=1 << 21), UNSUPPORTED), (dict(pages=-1), ARG), (dict(pages=1 << 31), UNSUPPORTED), (dict(pages=1 << 26), UNSUPPORTED), (dict(max_pages=-1), ARG),
     (dict(max_pages=1 << 28), UNSUPPORTED), (dict(slots=1), ARG), (dict(slot_idx=P, slots=0), ARG),
     (dict(rows=65536, slots=65536), UNSUPPORTED), (dict(window=-1), ARG), (dict(scale=float("nan")), ARG),
     (dict(scale=float("inf")), ARG), (dict(table=None), ARG), (dict(lens=None), ARG), (dict(q=None), ARG), (dict(out=None), ARG),
