@@ -118,6 +118,14 @@ cudaError_t f32(const PagedArgs& a, const Split& s, cudaStream_t st) {
                               sizeof(float) * HT * (16 * (D + 2) + D), st);
 }
 
+// More than 4 heads a key are taken in blocks of 4, whose second reading comes
+// from L2: 8 heads at once (8 dimensions a lane) took 64 rows of 8192 tokens from
+// 772 to 687 us, but 4 rows of 4096 tokens from 43 to 67 us.
+template <int D>
+cudaError_t f32(const PagedArgs& a, const Split& s, cudaStream_t st) {
+  return s.heads == 4 ? f32<D, 4>(a, s, st) : s.heads == 2 ? f32<D, 2>(a, s, st) : f32<D, 1>(a, s, st);
+}
+
 }  // namespace
 
 extern "C" {
@@ -172,10 +180,8 @@ int dl_paged_attention(const int* slot_idx, int slots, int rows, int Hq, int Hkv
   if (in_dtype == DL_BF16) {
     if (d == 128) e = s.heads == 8 ? bf16<128, 1, 1>(a, s, st) : bf16<128, 2, 1>(a, s, st);
     else e = s.heads == 8 ? bf16<64, 1, 2>(a, s, st) : bf16<64, 2, 2>(a, s, st);
-  } else if (d == 128) {
-    e = s.heads == 4 ? f32<128, 4>(a, s, st) : s.heads == 2 ? f32<128, 2>(a, s, st) : f32<128, 1>(a, s, st);
   } else {
-    e = s.heads == 4 ? f32<64, 4>(a, s, st) : s.heads == 2 ? f32<64, 2>(a, s, st) : f32<64, 1>(a, s, st);
+    e = d == 128 ? f32<128>(a, s, st) : f32<64>(a, s, st);
   }
   return e == cudaSuccess ? DL_OK : dl::launch_failed(e, "paged attention launch");
 }

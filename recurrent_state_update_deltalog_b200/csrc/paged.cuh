@@ -725,7 +725,7 @@ __global__ void __launch_bounds__(256) paged_write_kernel(PagedArgs a, int row_u
   const bool tell = blockIdx.x == 0 && threadIdx.x == 0;
   const int slot = row_slot(a.slot_idx, a.slots, r, a.err, tell);
   if (slot < 0) return;
-  const int s = __ldg(a.cu + r), e = __ldg(a.cu + r + 1), start = kPagedStarts ? __ldg(kPagedStarts + slot) : 0;
+  const int s = __ldg(a.cu + r), e = __ldg(a.cu + r + 1), start = a.starts ? __ldg(a.starts + slot) : 0;
   if (s < 0 || e < s || e > a.total || start < 0 ||
       static_cast<long long>(start) + e - s > (static_cast<long long>(a.max_pages) << a.page_shift)) {
     if (tell) raise_error(a.err, DL_DEVERR_SEQLEN);
