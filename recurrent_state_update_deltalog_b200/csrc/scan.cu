@@ -54,15 +54,26 @@ cudaError_t launch(const ScanArgs& a, int rows, int n, cudaStream_t st) {
   return dl::launch_cluster(kern, dim3(tiles * n, rows), dl::kScanThreads, smem, st, n, a, n);
 }
 
-// Stages of the ring.  One where rows average no more than one chunk: nothing
-// is left to load ahead, and more CTAs share an SM.  Three while the launch has
-// up to three CTAs an SM, else two, for the occupancy.
+template <typename TX, int V>
+cudaError_t launch_short(const ScanArgs& a, int rows, cudaStream_t st) {
+  dl::scan_short_kernel<TX, V><<<dim3((a.C + 128 * V - 1) / (128 * V), rows), 128, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+// Forward rows that average no more than one chunk take the short kernel.
+// Stages of the ring otherwise: one for such rows backwards (nothing is left to
+// load ahead, and more CTAs share an SM), three while the launch has up to three
+// CTAs an SM, else two, for the occupancy.
 template <bool BACK, typename TX, int MODE>
 cudaError_t launch(const ScanArgs& a, int rows, cudaStream_t st) {
+  const bool brief = a.total / rows <= dl::kScanChunk;
+  if constexpr (!BACK)
+    if (brief) return MODE == dl::WIDE ? launch_short<TX, 2>(a, rows, st) : launch_short<TX, 1>(a, rows, st);
   if constexpr (MODE == dl::NARROW) {
     return launch<BACK, TX, MODE, 2, false, 1>(a, rows, 1, st);
   } else {
-    if (a.total / rows <= dl::kScanChunk) return launch<BACK, TX, MODE, 2, false, 1>(a, rows, 1, st);
+    if constexpr (BACK)
+      if (brief) return launch<BACK, TX, MODE, 2, false, 1>(a, rows, 1, st);
     const long long units = (a.C + 63) / 64 * static_cast<long long>(rows);
     if (units < kSms) {
       const int n = cluster_of((a.C + 31) / 32, rows, a.total);

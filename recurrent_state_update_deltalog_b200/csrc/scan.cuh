@@ -511,6 +511,71 @@ __global__ void __launch_bounds__(kScanThreads) scan_backward_kernel(ScanArgs a,
   if (a.dh0 && rank == 0 && w == 0) store_row<MODE>(a.dh0 + row_at, carry, live);
 }
 
+// Short rows: a thread takes V neighbouring channels of a row through all its
+// tokens, eight at a time with the next eight on their way.  No exchange, no
+// tiles of 64 tokens of which most would be empty.
+template <typename TX, int V>
+__global__ void __launch_bounds__(128) scan_short_kernel(ScanArgs a) {
+  const int r = blockIdx.y;
+  const bool tell = blockIdx.x == 0 && threadIdx.x == 0;
+  const int c = (static_cast<int>(blockIdx.x) * 128 + static_cast<int>(threadIdx.x)) * V;
+  long long t0, n;
+  const int slot = row_slot(a.slot_idx, a.slots, r, a.err, tell);
+  if (slot < 0 || !scan_row(a, r, tell, &t0, &n) || c >= a.C) return;
+  const long long pool = static_cast<long long>(slot) * a.C + c;
+  float h[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) h[j] = a.h0 ? a.h0[pool + j] : 0.f;
+  const TX* px = static_cast<const TX*>(a.x) + t0 * a.C + c;
+  const float* pd = a.log_decay + t0 * a.C + c;
+  TX* po = static_cast<TX*>(a.h) + t0 * a.C + c;
+  constexpr int K = 8;
+  Pack<TX, V> x[K];
+  Pack<float, V> d[K];
+  auto load = [&](long long t) {
+#pragma unroll
+    for (int i = 0; i < K; ++i)
+      if (t + i < n) {
+        x[i] = load_stream<TX, V>(px + static_cast<long long>(i) * a.C);
+        d[i] = load_stream<float, V>(pd + static_cast<long long>(i) * a.C);
+      }
+    px += static_cast<long long>(K) * a.C;
+    pd += static_cast<long long>(K) * a.C;
+  };
+  load(0);
+  for (long long t = 0; t < n; t += K) {
+    Pack<TX, V> xs[K];
+    Pack<float, V> ds[K];
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      xs[i] = x[i];
+      ds[i] = d[i];
+    }
+    if (t + K < n) load(t + K);
+    if (a.ckpt && t % kScanChunk == 0) {
+      float* const to = a.ckpt + (t0 / kScanChunk + r + t / kScanChunk) * a.C + c;
+#pragma unroll
+      for (int j = 0; j < V; ++j) to[j] = h[j];
+    }
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      if (t + i < n) {
+        Pack<TX, V> o;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          h[j] = fmaf(decay_of(ds[i].v[j]), h[j], to_f32(xs[i].v[j]));
+          o.v[j] = from_f32<TX>(h[j]);
+        }
+        store_stream<TX, V>(po, o);
+      }
+      po += a.C;
+    }
+  }
+  if (a.h_last)
+#pragma unroll
+    for (int j = 0; j < V; ++j) a.h_last[pool + j] = h[j];
+}
+
 // One token for every row: h = exp(log_decay) state + x, rounded to the
 // output's type, and the fp32 state written back.  One thread for V channels;
 // grid (channel tiles, rows).
@@ -527,7 +592,7 @@ __global__ void __launch_bounds__(128) scan_step_kernel(ScanArgs a) {
   Pack<TX, V> o;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    h.v[j] = fmaf(expf(d.v[j]), h.v[j], to_f32(x.v[j]));
+    h.v[j] = fmaf(decay_of(d.v[j]), h.v[j], to_f32(x.v[j]));
     o.v[j] = from_f32<TX>(h.v[j]);
   }
   *reinterpret_cast<Pack<float, V>*>(a.h_last + st) = h;
