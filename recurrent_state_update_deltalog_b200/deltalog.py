@@ -115,23 +115,47 @@ class DeltaLog:
         self._check("u", u, (self.H, self.d_k), torch.float32)
         N.call("dl_set_bonus", self._h, _ptr(u), self._stream(stream))
 
-    def step(self, q, k, v, log_decay, beta=None, out=None, stream=None, slot_idx=None):
+    def _check_norm(self, norm_weight, gate, rows):
+        if norm_weight is None:
+            if gate is not None:
+                raise ValueError("gate goes with norm_weight")
+            return
+        self._check("norm_weight", norm_weight, (self.d_v,), torch.float32)
+        if gate is not None:
+            self._check("gate", gate, (self.B if rows is None else rows, self.H, self.d_v), self.dtype)
+
+    def _norm_out(self, out, norm_weight, gate, norm_eps, slot_idx, stream):
+        if norm_weight is not None:
+            from .ops import block_norm
+            with torch.no_grad():
+                block_norm(out, norm_weight, gate=gate, groups=self.H, eps=norm_eps, slot_idx=slot_idx,
+                           slots=self.B, out=out, stream=stream)
+
+    def step(self, q, k, v, log_decay, beta=None, out=None, stream=None, slot_idx=None, norm_weight=None,
+             gate=None, norm_eps=1e-6):
         """One DeltaLog decode token (append, or merge on the M-th step); returns o.
 
         With ``slot_idx`` (int32 [rows] on the device), inputs and output have
         ``rows`` batch rows and row r runs on slot ``slot_idx[r]`` (negative:
         padding row, left untouched); every live slot must be named, either
         active or held (``slot | DeltaLog.HOLD``: no input read, no output
-        written, state kept exactly)."""
+        written, state kept exactly).
+
+        With ``norm_weight`` (fp32 [d_v]) each head's output is normalised, scaled
+        and, with ``gate`` (like o), multiplied by silu(gate), in place
+        (:func:`~.ops.block_norm` with groups = H; o is rounded to its dtype
+        before).  Rows of padding and held slots stay as they were."""
         rows = self._slot_map(slot_idx)
         out = self._alloc_out(True, rows) if out is None else out
         self._check_step(q, k, v, log_decay, beta, out, True, rows)
+        self._check_norm(norm_weight, gate, rows)
         if rows is None:
             N.call("dl_step", self._h, _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(beta),
                    _ptr(out), self._stream(stream))
         else:
             N.call("dl_step_indexed", self._h, _ptr(slot_idx), rows, _ptr(q), _ptr(k), _ptr(v),
                    _ptr(log_decay), _ptr(beta), _ptr(out), self._stream(stream))
+        self._norm_out(out, norm_weight, gate, norm_eps, slot_idx, stream)
         return out
 
     def prefill(self, q, k, v, log_decay, beta=None, cu_seqlens=None, slot_idx=None,
