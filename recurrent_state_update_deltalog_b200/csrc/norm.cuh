@@ -654,7 +654,7 @@ __device__ __forceinline__ float load_weight(const float* p, int c, bool live) {
 
 // One channel a thread and step, NV steps.
 template <typename T, int NV, bool NARROW>
-__global__ void __launch_bounds__(NARROW ? kNormNarrow : NV == 8 ? 1024 : 512) norm_kernel(NormArgs a) {
+__global__ void __launch_bounds__(NARROW ? kNormNarrow : 1024, NARROW || NV > 2 ? 1 : 2) norm_kernel(NormArgs a) {
   __shared__ float sm[2][32][4];
   int turn = 0;
   const int lane = NARROW ? static_cast<int>(threadIdx.x) % a.tpr : static_cast<int>(threadIdx.x);
@@ -704,7 +704,7 @@ __global__ void __launch_bounds__(NARROW ? kNormNarrow : NV == 8 ? 1024 : 512) n
 
 // A CTA takes every gridDim.x-th row (narrow: 256 / tpr rows at a time).
 template <typename T, int NV, bool NARROW>
-__global__ void __launch_bounds__(NARROW ? kNormNarrow : NV == 8 ? 1024 : 512) norm_backward_kernel(NormArgs a) {
+__global__ void __launch_bounds__(NARROW ? kNormNarrow : 1024, NARROW || NV > 2 ? 1 : 2) norm_backward_kernel(NormArgs a) {
   __shared__ float sm[2][32][4];
   extern __shared__ float cols[];  // narrow: [256 / tpr][n] of one parameter at a time
   int turn = 0;
