@@ -59,6 +59,11 @@ struct NormArgs {
   float eps;
 };
 
+// Whether the slot map (if any: the division is not free) wants this row.
+__device__ __forceinline__ bool wanted(const NormArgs& a, long long row) {
+  return !a.slot_idx || row_slot(a.slot_idx, a.slots, static_cast<int>(row / a.groups), nullptr, false) >= 0;
+}
+
 // Sums K values over the threads of a row.  Narrow: `tpr` (8, 16 or 32) lanes.
 // Wide: the whole CTA, through `sm` [2][32][4], whose halves alternate between
 // calls so that one barrier a call is enough.
@@ -215,7 +220,7 @@ __global__ void __launch_bounds__(NARROW ? kNormNarrow : 512, NARROW ? 4 : 2) no
   ring.set(1, a.residual, a.y);
   if constexpr (GATE) ring.set(2, a.gate, a.y);
   auto here = [&](long long row) {
-    return row < a.rows && row_slot(a.slot_idx, a.slots, static_cast<int>(row / a.groups), nullptr, false) >= 0;
+    return row < a.rows && wanted(a, row);
   };
   long long first = static_cast<long long>(blockIdx.x) * per;
 #pragma unroll
@@ -660,7 +665,7 @@ __global__ void __launch_bounds__(NARROW ? kNormNarrow : 1024, NARROW || NV > 2 
   const int lane = NARROW ? static_cast<int>(threadIdx.x) % a.tpr : static_cast<int>(threadIdx.x);
   const long long row = NARROW ? static_cast<long long>(blockIdx.x) * (kNormNarrow / a.tpr) + threadIdx.x / a.tpr
                                : static_cast<long long>(blockIdx.x);
-  const bool here = row < a.rows && row_slot(a.slot_idx, a.slots, static_cast<int>(row / a.groups), nullptr, false) >= 0;
+  const bool here = row < a.rows && wanted(a, row);
   const float inv = 1.f / static_cast<float>(a.n);
   float y[NV], g[NV], o[NV], ss[1] = {0.f};
 #pragma unroll
