@@ -218,24 +218,26 @@ struct alignas(8 * PC) ScanMap {
 
 // The exchange of chunk totals in a cluster: at every step the last warp to
 // know its CTA's total sends it to all N CTAs (itself included), where the
-// bytes of N totals complete the step's mbarrier.  Two steps alternate between
-// two buffers: a CTA sends step s + 2 only after the others' step s + 1, which
-// they send only once all their warps have read step s.
+// bytes of N totals complete the step's mbarrier.  A CTA sends step s + 1 before
+// it waits for step s, so that the way there passes under work on the next
+// chunk.  Four buffers take turns: it sends step s + 2 after it has the others'
+// step s, which they sent after all their warps had read step s - 2.
 template <int PC>
 struct ScanExchange {
-  ScanMap<PC> tot[2][8][32];
-  uint64_t arrived[2];
+  static constexpr int B = 4;
+  ScanMap<PC> tot[B][8][32];
+  uint64_t arrived[B];
 
   __device__ __forceinline__ void start() {
     if (threadIdx.x == 0) {
-      mbar_init(&arrived[0], 1);
-      mbar_init(&arrived[1], 1);
+#pragma unroll
+      for (int i = 0; i < B; ++i) mbar_init(&arrived[i], 1);
       fence_mbar_init();
     }
     cluster_sync();  // every CTA of the cluster runs, and its barriers stand, before it is written to
   }
   __device__ __forceinline__ void send(int s, int N, int rank, const ScanMap<PC>& m) {
-    const int lane = threadIdx.x % 32, buf = s & 1;
+    const int lane = threadIdx.x % 32, buf = s % B;
     if (lane == 0) mbar_arrive_expect_tx(&arrived[buf], N * 32 * static_cast<int>(sizeof(m)));
     for (int q = 0; q < N; ++q) {
       const uint32_t to = remote_smem(&tot[buf][rank][lane], q), bar = remote_smem(&arrived[buf], q);
@@ -244,11 +246,14 @@ struct ScanExchange {
     }
   }
   __device__ __forceinline__ bool wait(int s, int* err) {
-    if (mbar_wait_bounded(&arrived[s & 1], (s >> 1) & 1)) return true;
+    if (mbar_wait_bounded(&arrived[s % B], s / B & 1)) return true;
     raise_error(err, DL_DEVERR_WAIT_TIMEOUT);
     return false;
   }
 };
+
+template <>
+struct ScanExchange<0> {};  // none
 
 // Grid (channel tiles * N, rows), clusters of N along x; PC channels a lane; a
 // ring of S stages.
@@ -258,7 +263,7 @@ __global__ void __launch_bounds__(kScanThreads) scan_kernel(ScanArgs a, int N) {
   extern __shared__ __align__(16) unsigned char ring_bytes[];
   Stage* const ring = reinterpret_cast<Stage*>(ring_bytes);
   __shared__ ScanMap<PC> part[kScanWarps][32];  // each warp's tokens
-  __shared__ ScanExchange<PC> ex;
+  __shared__ ScanExchange<CLUSTER ? PC : 0> ex;
 
   const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int rank = CLUSTER ? static_cast<int>(cluster_rank()) : 0;
@@ -291,61 +296,49 @@ __global__ void __launch_bounds__(kScanThreads) scan_kernel(ScanArgs a, int N) {
   for (int s = 0; s < S - 1 + (S == 1); ++s) issue(s);
   if constexpr (CLUSTER) ex.start();
 
-  for (int s = 0; s < steps; ++s) {
-    const long long t = s * stride + mine + w * kScanTok;
+  // One chunk: its decays and inputs, and what the CTA's warps before this one do.
+  struct Chunk {
+    float al[kScanTok][PC];
+    Pack<TX, PC> x[kScanTok];
+    ScanMap<PC> before, own;
+  };
+  auto begin = [&](int s, Chunk& k) {
     copy_wait<S == 1 ? 0 : S - 2>();
     __syncthreads();  // stage s is here for all warps, and all have left the stage before it and `part`
     if constexpr (S > 1) issue(s + S - 1);
-
     const Stage& st = ring[s % S];
     const unsigned first = static_cast<unsigned>((t0 + s * stride + mine) * a.C + c0);
-    float al[kScanTok][PC];
-    Pack<TX, PC> x[kScanTok];
-    ScanMap<PC> own;
-    own.identity();
+    k.own.identity();
 #pragma unroll
     for (int i = 0; i < kScanTok; ++i) {
       const Pack<float, PC> d = st.d.get(w * kScanTok + i, lane, first, a.C);
-      x[i] = st.x.get(w * kScanTok + i, lane, first, a.C);
+      k.x[i] = st.x.get(w * kScanTok + i, lane, first, a.C);
 #pragma unroll
       for (int j = 0; j < PC; ++j) {
-        al[i][j] = decay_of(d.v[j]);
-        own.b[j] = fmaf(al[i][j], own.b[j], to_f32(x[i].v[j]));
-        own.A[j] *= al[i][j];
+        k.al[i][j] = decay_of(d.v[j]);
+        k.own.b[j] = fmaf(k.al[i][j], k.own.b[j], to_f32(k.x[i].v[j]));
+        k.own.A[j] *= k.al[i][j];
       }
     }
-    part[w][lane] = own;
+    part[w][lane] = k.own;
     __syncthreads();
     if constexpr (S == 1) issue(s + 1);
-
-    ScanMap<PC> before;  // the chunk's warps before this one
-    before.identity();
-    for (int i = 0; i < w; ++i) before.then(part[i][lane]);
-    float h[PC];  // state before this chunk
-#pragma unroll
-    for (int j = 0; j < PC; ++j) h[j] = carry[j];
+    k.before.identity();
+    for (int i = 0; i < w; ++i) k.before.then(part[i][lane]);
     if constexpr (CLUSTER) {
       if (w == kScanWarps - 1) {
-        ScanMap<PC> all = before;
-        all.then(own);
+        ScanMap<PC> all = k.before;
+        all.then(k.own);
         ex.send(s, N, rank, all);
       }
-      if (!ex.wait(s, a.err)) break;
-      for (int q = 0; q < N; ++q) {
-        if (q == rank) {
-#pragma unroll
-          for (int j = 0; j < PC; ++j) h[j] = carry[j];
-        }
-        ex.tot[s & 1][q][lane].apply(carry);
-      }
-    } else {
-      ScanMap<PC> all = before;
-      for (int i = w; i < kScanWarps; ++i) all.then(part[i][lane]);
-      all.apply(carry);
     }
+  };
+  // Its outputs, from the state h before it.
+  auto end = [&](int s, Chunk& k, float (&h)[PC]) {
+    const long long t = s * stride + mine + w * kScanTok;
     if (a.ckpt && w == 0 && t < n)
       store_row<MODE>(a.ckpt + (t0 / kScanChunk + r + t / kScanChunk) * a.C + c, h, live);
-    before.apply(h);
+    k.before.apply(h);
     TX* po = out + (t0 + t) * a.C + c;
     const int left = static_cast<int>(n - t < kScanTok ? n - t : kScanTok);
 #pragma unroll
@@ -353,11 +346,40 @@ __global__ void __launch_bounds__(kScanThreads) scan_kernel(ScanArgs a, int N) {
       Pack<TX, PC> o;
 #pragma unroll
       for (int j = 0; j < PC; ++j) {
-        h[j] = fmaf(al[i][j], h[j], to_f32(x[i].v[j]));
+        h[j] = fmaf(k.al[i][j], h[j], to_f32(k.x[i].v[j]));
         o.v[j] = from_f32<TX>(h[j]);
       }
       if (i < left) store_out<MODE>(po, o, live);
       po += a.C;
+    }
+  };
+  Chunk now;
+  float h[PC];
+  if constexpr (CLUSTER) {
+    Chunk next;
+    if (steps > 0) begin(0, now);
+    for (int s = 0; s < steps; ++s) {
+      if (s + 1 < steps) begin(s + 1, next);
+      if (!ex.wait(s, a.err)) break;
+      for (int q = 0; q < N; ++q) {
+        if (q == rank) {
+#pragma unroll
+          for (int j = 0; j < PC; ++j) h[j] = carry[j];
+        }
+        ex.tot[s % ex.B][q][lane].apply(carry);
+      }
+      end(s, now, h);
+      now = next;
+    }
+  } else {
+    for (int s = 0; s < steps; ++s) {
+      begin(s, now);
+      ScanMap<PC> all = now.before;
+      for (int i = w; i < kScanWarps; ++i) all.then(part[i][lane]);
+#pragma unroll
+      for (int j = 0; j < PC; ++j) h[j] = carry[j];
+      all.apply(carry);
+      end(s, now, h);
     }
   }
   copy_wait<0>();
@@ -379,7 +401,7 @@ __global__ void __launch_bounds__(kScanThreads) scan_backward_kernel(ScanArgs a,
   extern __shared__ __align__(16) unsigned char ring_bytes[];
   Stage* const ring = reinterpret_cast<Stage*>(ring_bytes);
   __shared__ ScanMap<PC> part[kScanWarps][32], back[kScanWarps][32];  // each warp's tokens, forwards and backwards
-  __shared__ ScanExchange<PC> ex;
+  __shared__ ScanExchange<CLUSTER ? PC : 0> ex;
 
   const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int rank = CLUSTER ? static_cast<int>(cluster_rank()) : 0;
@@ -412,31 +434,35 @@ __global__ void __launch_bounds__(kScanThreads) scan_backward_kernel(ScanArgs a,
   for (int k = 0; k < S - 1 + (S == 1); ++k) issue(k);
   if constexpr (CLUSTER) ex.start();
 
-  for (int k = 0; k < steps; ++k) {
-    const long long chunk = (steps - 1 - k) * static_cast<long long>(N) + rank, t = chunk * kScanChunk + w * kScanTok;
-    float h[PC];  // state before this chunk
-    load_row<MODE>(h, chunk * kScanChunk < n ? a.ckpt + (t0 / kScanChunk + r + chunk) * a.C + c : nullptr, live);
+  // One chunk: its decays, inputs and gradients, the state h before this warp's
+  // tokens, and what the CTA's warps behind this one do to R.
+  struct Chunk {
+    float al[kScanTok][PC], h[PC];
+    Pack<TX, PC> x[kScanTok], g[kScanTok];
+    ScanMap<PC> behind;
+  };
+  auto chunk_of = [&](int k) { return (steps - 1 - k) * static_cast<long long>(N) + rank; };
+  auto begin = [&](int k, Chunk& q) {
+    const long long chunk = chunk_of(k);
+    load_row<MODE>(q.h, chunk * kScanChunk < n ? a.ckpt + (t0 / kScanChunk + r + chunk) * a.C + c : nullptr, live);
     copy_wait<S == 1 ? 0 : S - 2>();
     __syncthreads();
     if constexpr (S > 1) issue(k + S - 1);
-
     const Stage& st = ring[k % S];
     const unsigned first = static_cast<unsigned>((t0 + chunk * kScanChunk) * a.C + c0);
-    float al[kScanTok][PC];
-    Pack<TX, PC> x[kScanTok], g[kScanTok];
     ScanMap<PC> own, own_back;
     own.identity();
     own_back.identity();
 #pragma unroll
     for (int i = 0; i < kScanTok; ++i) {
       const Pack<float, PC> d = st.d.get(w * kScanTok + i, lane, first, a.C);
-      x[i] = st.x.get(w * kScanTok + i, lane, first, a.C);
-      g[i] = st.g.get(w * kScanTok + i, lane, first, a.C);
+      q.x[i] = st.x.get(w * kScanTok + i, lane, first, a.C);
+      q.g[i] = st.g.get(w * kScanTok + i, lane, first, a.C);
 #pragma unroll
       for (int j = 0; j < PC; ++j) {
-        al[i][j] = decay_of(d.v[j]);
-        own.b[j] = fmaf(al[i][j], own.b[j], to_f32(x[i].v[j]));
-        own.A[j] *= al[i][j];
+        q.al[i][j] = decay_of(d.v[j]);
+        own.b[j] = fmaf(q.al[i][j], own.b[j], to_f32(q.x[i].v[j]));
+        own.A[j] *= q.al[i][j];
       }
     }
 #pragma unroll
@@ -444,46 +470,33 @@ __global__ void __launch_bounds__(kScanThreads) scan_backward_kernel(ScanArgs a,
 #pragma unroll
     for (int i = kScanTok - 1; i >= 0; --i)
 #pragma unroll
-      for (int j = 0; j < PC; ++j) own_back.b[j] = al[i][j] * (to_f32(g[i].v[j]) + own_back.b[j]);
+      for (int j = 0; j < PC; ++j) own_back.b[j] = q.al[i][j] * (to_f32(q.g[i].v[j]) + own_back.b[j]);
     part[w][lane] = own;
     back[w][lane] = own_back;
     __syncthreads();
     if constexpr (S == 1) issue(k + 1);
-
-    for (int i = 0; i < w; ++i) part[i][lane].apply(h);  // state before this warp's tokens
-    ScanMap<PC> behind;                                  // the chunk's warps behind this one
-    behind.identity();
-    for (int i = kScanWarps - 1; i > w; --i) behind.then(back[i][lane]);
-    float R[PC];
-#pragma unroll
-    for (int j = 0; j < PC; ++j) R[j] = carry[j];
+    for (int i = 0; i < w; ++i) part[i][lane].apply(q.h);
+    q.behind.identity();
+    for (int i = kScanWarps - 1; i > w; --i) q.behind.then(back[i][lane]);
     if constexpr (CLUSTER) {
       if (w == 0) {
-        ScanMap<PC> all = behind;
+        ScanMap<PC> all = q.behind;
         all.then(own_back);
         ex.send(k, N, rank, all);
       }
-      if (!ex.wait(k, a.err)) break;
-      for (int q = N - 1; q >= 0; --q) {
-        if (q == rank) {
-#pragma unroll
-          for (int j = 0; j < PC; ++j) R[j] = carry[j];
-        }
-        ex.tot[k & 1][q][lane].apply(carry);
-      }
-    } else {
-      ScanMap<PC> all = behind;
-      for (int i = w; i >= 0; --i) all.then(back[i][lane]);
-      all.apply(carry);
     }
-    behind.apply(R);
+  };
+  // Its gradients, from R behind it.
+  auto end = [&](int k, Chunk& q, float (&R)[PC]) {
+    const long long t = chunk_of(k) * kScanChunk + w * kScanTok;
+    q.behind.apply(R);
     float hp[kScanTok][PC];  // a_t h_{t-1}
 #pragma unroll
     for (int i = 0; i < kScanTok; ++i)
 #pragma unroll
       for (int j = 0; j < PC; ++j) {
-        hp[i][j] = al[i][j] * h[j];
-        h[j] = hp[i][j] + to_f32(x[i].v[j]);
+        hp[i][j] = q.al[i][j] * q.h[j];
+        q.h[j] = hp[i][j] + to_f32(q.x[i].v[j]);
       }
     const int left = static_cast<int>(n - t < kScanTok ? n - t : kScanTok);
     TX* ox = dx + (t0 + t + kScanTok - 1) * a.C + c;
@@ -494,10 +507,10 @@ __global__ void __launch_bounds__(kScanThreads) scan_backward_kernel(ScanArgs a,
       Pack<float, PC> vd;
 #pragma unroll
       for (int j = 0; j < PC; ++j) {
-        const float G = to_f32(g[i].v[j]) + R[j];
+        const float G = to_f32(q.g[i].v[j]) + R[j];
         vx.v[j] = from_f32<TX>(G);
         vd.v[j] = hp[i][j] * G;
-        R[j] = al[i][j] * G;
+        R[j] = q.al[i][j] * G;
       }
       if (i < left) {
         store_out<MODE>(ox, vx, live);
@@ -505,6 +518,35 @@ __global__ void __launch_bounds__(kScanThreads) scan_backward_kernel(ScanArgs a,
       }
       ox -= a.C;
       od -= a.C;
+    }
+  };
+  Chunk now;
+  float R[PC];
+  if constexpr (CLUSTER) {
+    Chunk next;
+    if (steps > 0) begin(0, now);
+    for (int k = 0; k < steps; ++k) {
+      if (k + 1 < steps) begin(k + 1, next);
+      if (!ex.wait(k, a.err)) break;
+      for (int q = N - 1; q >= 0; --q) {
+        if (q == rank) {
+#pragma unroll
+          for (int j = 0; j < PC; ++j) R[j] = carry[j];
+        }
+        ex.tot[k % ex.B][q][lane].apply(carry);
+      }
+      end(k, now, R);
+      now = next;
+    }
+  } else {
+    for (int k = 0; k < steps; ++k) {
+      begin(k, now);
+      ScanMap<PC> all = now.behind;
+      for (int i = w; i >= 0; --i) all.then(back[i][lane]);
+#pragma unroll
+      for (int j = 0; j < PC; ++j) R[j] = carry[j];
+      all.apply(carry);
+      end(k, now, R);
     }
   }
   copy_wait<0>();
