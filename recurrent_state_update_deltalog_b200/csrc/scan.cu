@@ -20,12 +20,13 @@ int mode_of(int C, int dtype, std::initializer_list<const void*> tensors) {
   return C % (dtype == DL_BF16 ? 8 : 4) ? dl::SHIFT : dl::WIDE;
 }
 
-// CTAs along time: as many as it takes to give every SM one, if the sequences
-// have that many chunks of 64 tokens on average.
-int cluster_of(long long tiles, int rows, long long total) {
+// CTAs along time: as many as it takes to give the launch `want`, if the sequences have
+// that many chunks of 64 tokens on average.  16 is more than every device
+// promises, and this one has.
+int cluster_of(long long tiles, int rows, long long total, int want) {
   const long long chunks = (total / rows + dl::kScanChunk - 1) / dl::kScanChunk;
   int n = 1;
-  while (n < 8 && 2 * n <= chunks && tiles * rows * n < kSms) n *= 2;
+  while (n < dl::kScanCluster && 2 * n <= chunks && tiles * rows * n < (n < 8 ? want : kSms)) n *= 2;
   return n;
 }
 
@@ -51,6 +52,10 @@ cudaError_t launch(const ScanArgs& a, int rows, int n, cudaStream_t st) {
   const int smem = S * (BACK ? sizeof(dl::ScanBackStage<TX, MODE, PC>) : sizeof(dl::ScanStage<TX, MODE, PC>));
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
+  if (n > 8) {
+    const cudaError_t f = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (f != cudaSuccess) return f;
+  }
   return dl::launch_cluster(kern, dim3(tiles * n, rows), dl::kScanThreads, smem, st, n, a, n);
 }
 
@@ -76,7 +81,9 @@ cudaError_t launch(const ScanArgs& a, int rows, cudaStream_t st) {
       if (brief) return launch<BACK, TX, MODE, 2, false, 1>(a, rows, 1, st);
     const long long units = (a.C + 63) / 64 * static_cast<long long>(rows);
     if (units < kSms) {
-      const int n = cluster_of((a.C + 31) / 32, rows, a.total);
+      // a CTA an SM, and two of the light bf16 forward ones (1 x 16384 x 4096 173 ->
+      // 123 us; fp32 161 -> 176, backward 237 -> 236)
+      const int n = cluster_of((a.C + 31) / 32, rows, a.total, !BACK && sizeof(TX) == 2 ? 2 * kSms : kSms);
       return n > 1 ? launch<BACK, TX, MODE, 1, true, 3>(a, rows, n, st) : launch<BACK, TX, MODE, 1, false, 3>(a, rows, 1, st);
     }
     return units <= 3 * kSms ? launch<BACK, TX, MODE, 2, false, 3>(a, rows, 1, st)

@@ -30,6 +30,7 @@ constexpr int kScanWarps = 4;                      // warps of a CTA, consecutiv
 constexpr int kScanTok = 16;                       // tokens of a warp, in registers
 constexpr int kScanChunk = kScanWarps * kScanTok;  // tokens of a CTA
 constexpr int kScanThreads = kScanWarps * 32;
+constexpr int kScanCluster = 16;  // most CTAs of a cluster
 static_assert(kScanChunk == DL_SCAN_CHUNK, "checkpoint interval of the interface");
 
 struct ScanArgs {
@@ -225,7 +226,7 @@ struct alignas(8 * PC) ScanMap {
 template <int PC>
 struct ScanExchange {
   static constexpr int B = 4;
-  ScanMap<PC> tot[B][8][32];
+  ScanMap<PC> tot[B][kScanCluster][32];
   uint64_t arrived[B];
 
   __device__ __forceinline__ void start() {
