@@ -20,9 +20,10 @@ int mode_of(int C, int dtype, std::initializer_list<const void*> tensors) {
   return C % (dtype == DL_BF16 ? 8 : 4) ? dl::SHIFT : dl::WIDE;
 }
 
-// CTAs along time: as many as it takes to give the launch `want`, if the sequences have
-// that many chunks of 64 tokens on average.  16 is more than every device
-// promises, and this one has.
+// CTAs along time: as many as it takes to give the launch `want`, if the sequences
+// have that many chunks of 64 tokens on average; 16 only if 8 leave SMs idle
+// (1 x 32768 x 128 fp32 68 -> 38 us; but 1 x 16384 x 1024 bf16 50 -> 59 us: clusters
+// of 16 find room for fewer CTAs).
 int cluster_of(long long tiles, int rows, long long total, int want) {
   const long long chunks = (total / rows + dl::kScanChunk - 1) / dl::kScanChunk;
   int n = 1;

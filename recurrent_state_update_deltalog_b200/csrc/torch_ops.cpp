@@ -245,7 +245,8 @@ NormSizes norm_check(const Tensor& y, const OptTensor& post, const OptTensor& ga
   const int dt = check_first("y", y);
   TORCH_CHECK_VALUE(y.dim() >= 1, "y must have a dimension");
   int64_t D = y.size(-1);
-  if (groups > 1 && y.dim() >= 3 && y.size(-2) == groups) D *= groups;  // [..., H, d]: the groups are a dimension
+  // [..., H, d]: the groups are a dimension, unless the weight says that the last one holds them
+  if (groups > 1 && y.dim() >= 3 && y.size(-2) == groups && (!post || post->numel() * groups != D)) D *= groups;
   TORCH_CHECK_VALUE(groups >= 1 && D >= 1 && D % groups == 0, "the last dimension (", D, ") must be a positive multiple of groups (", groups, ")");
   check("gate", gate, y.sizes(), y.scalar_type(), y.device());
   check("residual", residual, y.sizes(), y.scalar_type(), y.device());

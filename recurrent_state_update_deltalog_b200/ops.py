@@ -127,7 +127,7 @@ def block_norm(y, post_weight=None, gate=None, scale=None, residual=None, pre_we
     silu(gate), times scale; out = residual + u; normed = RMSNorm(out) * pre_weight.
     Every part but y may be None.  y, gate, residual are bf16 or fp32 [..., D]; weights
     fp32: post_weight [D / groups], scale and pre_weight [D] (groups = 1 only).  With
-    ``groups = H`` y may also be [..., H, d].  Returns out, or (out, normed) with a
+    ``groups = H`` y may also be [..., H, d], post_weight [d].  Returns out, or (out, normed) with a
     pre_weight; differentiable in every part (first derivatives).
 
     Serving (no gradients): ``out`` and ``normed_out`` may be y, gate or residual (in

@@ -304,3 +304,15 @@ def test_no_second_derivative_and_no_graph_without_need():
     gated_scan_step(torch.zeros(2, 16, device="cuda"), torch.zeros(2, 16, device="cuda"), pool)
     with pytest.raises(RuntimeError, match="modified by an inplace"):
         y.backward()
+
+
+def test_groups_as_a_dimension_or_inside_the_last():
+    """[T, H, d] with a weight [d] is [T, H d]; [T, H, D] with a weight [D / H] keeps its groups in the last dimension."""
+    from recurrent_state_update_deltalog_b200 import block_norm
+    t = make(6, 8 * 64, 8, torch.float32, 17, ("post_weight", "gate"))
+    y, gate, w = t["y"].cuda(), t["gate"].cuda(), t["post_weight"].cuda()
+    want = block_norm(y, w, gate=gate, groups=8)
+    assert torch.equal(block_norm(y.view(6, 8, 64), w, gate=gate.view(6, 8, 64), groups=8).view_as(y), want)
+    y3 = y.repeat_interleave(8, 0).view(6, 8, 512)
+    got = block_norm(y3, w, gate=gate.repeat_interleave(8, 0).view(6, 8, 512), groups=8)
+    assert torch.equal(got, want.repeat_interleave(8, 0).view(6, 8, 512))

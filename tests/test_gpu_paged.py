@@ -128,6 +128,55 @@ def test_long_rows_split_over_clusters(lens, dtype):
 
 
 @pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("d,page,Hkv,G,window", [(128, 16, 2, 4, 0), (64, 8, 2, 4, 4700), (128, 64, 1, 12, 4700), (64, 1, 1, 9, 0),
+                                                 (128, 8, 1, 17, 5001), (64, 128, 3, 1, 0)])
+def test_evenly_shared_tables(d, page, Hkv, G, window, dtype):
+    """Tables long enough that equal runs of all tiles are dealt out: empty, short and long rows, some of them cut,
+    windows that start inside a tile, pages smaller than a tile; with and without the new token."""
+    from recurrent_state_update_deltalog_b200 import _native as N
+    import ctypes
+    lens = [9000, 0, 4500, 17, 6001, 1, 0, 333]
+    c = make(lens, Hkv, G, d, page, dtype, 11, spare_slots=2)
+    need = ctypes.c_size_t()
+    N.call("dl_paged_attention_workspace", len(lens), Hkv * G, Hkv, d, 1 if dtype == torch.bfloat16 else 0, page, c["table"].shape[1],
+           window, ctypes.byref(need))
+    assert need.value > 0
+    for new in (True, False):
+        check(c, G, window, dtype, new)
+
+
+def test_evenly_shared_tables_captured_and_skipped():
+    """The two launches of that form in a captured graph, with lengths changed between replays; rows of negative, held
+    and too large slots are not written."""
+    from recurrent_state_update_deltalog_b200 import DeltaLog, DeltaLogError, check_errors, paged_attention
+    c = make([9000, 5000, 40, 7000], 2, 4, 128, 16, torch.bfloat16, 12)
+    dev = {k: c[k].cuda() for k in ("q", "kp", "vp", "table", "lens")}
+    slot = c["slot"].clone()
+    slot[1], slot[3] = -1, int(slot[3]) | DeltaLog.HOLD
+    slot = slot.cuda()
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    live, out = dev["lens"].clone(), torch.full_like(dev["q"], 3.0)
+    args = (dev["q"], dev["kp"], dev["vp"], dev["table"])
+    want = [paged_attention(*args, n, slot_idx=slot, out=torch.full_like(out, 3.0)) for n in (dev["lens"], dev["lens"] - 39)]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        paged_attention(*args, live, slot_idx=slot, out=out, err=err)
+    for n, w in ((dev["lens"] - 39, want[1]), (dev["lens"], want[0])):
+        live.copy_(n)
+        out.fill_(3.0)
+        g.replay()
+        assert torch.equal(out, w) and (out[[1, 3]] == 3.0).all()
+    check_errors(err)
+    ref, bound = reference(c, 4, 0, 128 ** -0.5, torch.bfloat16)
+    i = [0, 2]
+    assert_within(out[i], ref[i], rounded(bound, ref, torch.bfloat16)[i], "o")
+    slot[2] = 4
+    with pytest.raises(DeltaLogError, match="slot index"):
+        paged_attention(*args, dev["lens"], slot_idx=slot, err=err)
+        check_errors(err)
+
+
+@pytest.mark.parametrize("dtype", DT)
 def test_long_rows_without_a_workspace(dtype):
     """The C call without a workspace splits less, over one cluster; the values stay within the same bounds."""
     import ctypes
