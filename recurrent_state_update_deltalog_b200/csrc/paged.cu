@@ -102,7 +102,7 @@ cudaError_t launch(Kernel clusters, Kernel even, const PagedArgs& a, const Split
   const dim3 heads(a.Hkv * a.G, a.rows);
   // few units: each is cut into many pieces
   return static_cast<long long>(a.rows) * a.Hkv * s.head_blocks < kSms
-             ? dl::launch_maybe_pdl(dl::paged_join_kernel<T, D, HT, 4>, heads, 4 * D, 0, st, true, a)
+             ? dl::launch_maybe_pdl(dl::paged_join_kernel<T, D, HT, 8>, heads, 8 * D, 0, st, true, a)
              : dl::launch_maybe_pdl(dl::paged_join_kernel<T, D, HT, 1>, heads, D, 0, st, true, a);
 }
 
