@@ -10,6 +10,7 @@ using dl::NormArgs;
 int bad(const char* msg) { return dl::record_error(DL_ERR_ARG, msg); }
 
 constexpr int kSms = 148;
+constexpr int kAhead = 220 * 1024;  // shared memory of an SM for rows on their way
 
 // How a row of n channels lies on threads: V channels a piece (16 bytes, or
 // one channel where rows start on any address), nv pieces a thread, tpr
@@ -17,11 +18,13 @@ constexpr int kSms = 148;
 struct Shape {
   int vec, nv, tpr;
   bool narrow;
+  int ahead;  // rows on any address: bytes of the next rows' places in a CTA, 0 for none
   int block() const { return narrow ? dl::kNormNarrow : tpr; }
   int rows_per_cta() const { return narrow ? dl::kNormNarrow / tpr : 1; }
 };
 
-Shape shape_of(int n, int dtype, bool aligned, bool back) {
+// `at16`: the tensors start on 16 bytes; `tensors`: how many are read.
+Shape shape_of(long long rows, int n, int dtype, bool aligned, bool at16, int tensors, bool back) {
   Shape s{};
   s.vec = aligned ? (dtype == DL_BF16 ? 8 : 4) : 1;
   const int pieces = (n + s.vec - 1) / s.vec;
@@ -37,21 +40,38 @@ Shape shape_of(int n, int dtype, bool aligned, bool back) {
   } else {
     s.tpr = ((pieces + s.nv - 1) / s.nv + 31) / 32 * 32;
   }
+  // Many rows on any address, n small: the next row on its way (norm.cuh), a warp
+  // a row up to 256 channels.  With / without, forward and backward, us: 100000 x 131
+  // fp32 63 + 152 / 126 + 236; 40000 x 333 bf16 76 + 138 / 118 + 220; backward 20000 x
+  // 1001 bf16 218 / 298.  Not so 300000 x 31 (128 + 207 / 92 + 147), 30000 x 601
+  // forward (114 / 106), 12000 x 2051 backward (341 / 287 in fp32) or few rows (64 x 163
+  // 2.9 + 7.0 / 2.4 + 5.1; 3000 x 1111 backward 49 / 47).
+  if (!aligned && at16 && rows >= 20 * kSms && n > 32 && n <= (back ? 2048 : 512)) {
+    s.narrow = n <= 256;
+    s.nv = s.narrow ? (n <= 64 ? 2 : n <= 96 ? 3 : n <= 128 ? 4 : n <= 192 ? 6 : 8) : n <= 512 ? 4 : 8;
+    s.tpr = s.narrow ? 32 : ((n + s.nv - 1) / s.nv + 31) / 32 * 32;
+    const int units = dtype == DL_BF16 ? dl::ahead_units<__nv_bfloat16>(n) : dl::ahead_units<float>(n);
+    s.ahead = 2 * tensors * units * 16 * s.rows_per_cta();  // at most 83 KB
+  }
   return s;
 }
 
-// Whether every row of every tensor starts on 16 bytes, and the weights do.
-bool aligned_rows(int n, int dtype, std::initializer_list<const void*> pointers) {
-  if (n % (dtype == DL_BF16 ? 8 : 4)) return false;
+bool aligned16(std::initializer_list<const void*> pointers) {
   for (const void* p : pointers)
     if (!dl::is_aligned(p, 16)) return false;
   return true;
 }
 
+// Whether every row of every tensor starts on 16 bytes, and the weights do.
+bool aligned_rows(int n, int dtype, std::initializer_list<const void*> pointers) {
+  return n % (dtype == DL_BF16 ? 8 : 4) == 0 && aligned16(pointers);
+}
+
 // CTAs of a kernel that stays and takes row after row: as many as the SMs hold
 // (by its launch bounds), no more than there are rows.
 int staying_ctas(long long rows, const Shape& s, bool back) {
-  const int per_sm = s.narrow ? (back ? 2 : 4) : (s.vec == 1 ? (s.nv <= 2 ? 2048 : 1024) : back ? 512 : 1024) / s.tpr;
+  int per_sm = s.narrow ? (back ? 2 : s.ahead ? 3 : 4) : (s.vec == 1 && !s.ahead ? (s.nv <= 2 ? 2048 : 1024) : back ? 512 : 1024) / s.tpr;
+  if (s.ahead && per_sm > kAhead / s.ahead) per_sm = kAhead / s.ahead;
   const long long need = (rows + s.rows_per_cta() - 1) / s.rows_per_cta();
   const long long most = static_cast<long long>(kSms) * (per_sm < 1 ? 1 : per_sm > 8 ? 8 : per_sm);
   return static_cast<int>(need < most ? need : most);
@@ -130,6 +150,19 @@ cudaError_t run_any(const NormArgs& a, const Shape& s, int ctas, bool back, cuda
   return cudaGetLastError();
 }
 
+template <typename T, int NV, bool NARROW>
+cudaError_t run_ahead(const NormArgs& a, const Shape& s, int ctas, bool back, cudaStream_t st) {
+  auto kern = dl::norm_backward_ahead_kernel<T, NV, NARROW>;
+  if constexpr (NARROW || NV == 4)
+    if (!back) kern = dl::norm_ahead_kernel<T, NV, NARROW>;
+  if (s.ahead > 40 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, s.ahead);
+    if (e != cudaSuccess) return e;
+  }
+  kern<<<ctas, s.block(), s.ahead, st>>>(a);
+  return cudaGetLastError();
+}
+
 template <typename T>
 cudaError_t run(const NormArgs& a, const Shape& s, int ctas, bool back, cudaStream_t st) {
   if (s.vec > 1) {
@@ -141,6 +174,16 @@ cudaError_t run(const NormArgs& a, const Shape& s, int ctas, bool back, cudaStre
         if constexpr (sizeof(T) == 4) return run_ring<T, 4, false>(a, s, ctas, back, st);
     }
     return cudaErrorInvalidValue;
+  }
+  if (s.ahead) {
+    if (!s.narrow) return s.nv == 4 ? run_ahead<T, 4, false>(a, s, ctas, back, st) : run_ahead<T, 8, false>(a, s, ctas, back, st);
+    switch (s.nv) {
+      case 2: return run_ahead<T, 2, true>(a, s, ctas, back, st);
+      case 3: return run_ahead<T, 3, true>(a, s, ctas, back, st);
+      case 4: return run_ahead<T, 4, true>(a, s, ctas, back, st);
+      case 6: return run_ahead<T, 6, true>(a, s, ctas, back, st);
+      default: return run_ahead<T, 8, true>(a, s, ctas, back, st);
+    }
   }
   if (s.narrow) return run_any<T, 1, true>(a, s, ctas, back, st);
   switch (s.nv) {
@@ -187,7 +230,8 @@ int dl_block_norm(const int* slot_idx, int slots, int rows, int D, int groups, i
   a.n = D / groups;
   a.rows = static_cast<long long>(rows) * groups;
   a.eps = eps;
-  const Shape s = shape_of(a.n, in_dtype, aligned_rows(a.n, in_dtype, {y, gate, residual, out, normed, post_weight, scale, pre_weight}), false);
+  const Shape s = shape_of(a.rows, a.n, in_dtype, aligned_rows(a.n, in_dtype, {y, gate, residual, out, normed, post_weight, scale, pre_weight}),
+                           aligned16({y, gate, residual}), 1 + !!gate + !!residual, false);
   a.tpr = s.tpr;
   const int ctas = staying_ctas(a.rows, s, false);
   const cudaError_t e = run(a, s, ctas, in_dtype, false, static_cast<cudaStream_t>(stream));
@@ -240,7 +284,8 @@ int dl_block_norm_backward(int rows, int D, int groups, int in_dtype, const void
     a.n = n;
     a.rows = static_cast<long long>(rows) * groups;
     a.eps = eps;
-    const Shape s = shape_of(n, in_dtype, aligned_rows(n, in_dtype, {y, gate, residual, dout, dnormed, dy, dgate, dresidual, post_weight, scale, pre_weight}), true);
+    const Shape s = shape_of(a.rows, n, in_dtype, aligned_rows(n, in_dtype, {y, gate, residual, dout, dnormed, dy, dgate, dresidual, post_weight, scale, pre_weight}),
+                             aligned16({y, gate, residual, dout, dnormed}), 1 + !!gate + !!dout + (pre_weight && residual) + !!dnormed, true);
     a.tpr = s.tpr;
     ctas = staying_ctas(a.rows, s, true);
     e = run(a, s, ctas, in_dtype, true, st);

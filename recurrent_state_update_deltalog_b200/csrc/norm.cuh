@@ -23,8 +23,8 @@
 // row: a thread's 16-byte pieces of the rows to come travel by cp.async into
 // its own places of a shared memory ring, which no other thread reads, so the
 // ring needs no barrier; weights and parameter sums stay in registers; fp32
-// operations come in pairs.  Rows that do not start on 16 bytes are read element
-// by element, one row at a time.
+// operations come in pairs.  Rows that do not start on 16 bytes go element by
+// element, through shared memory where they are many.
 #pragma once
 
 #include "ops.cuh"
@@ -32,6 +32,11 @@
 namespace dl {
 
 constexpr int kNormMax = 8192;  // channels of a row
+// 16-byte units that cover a row of n channels on any address.
+template <typename T>
+__host__ __device__ constexpr int ahead_units(int n) {
+  return (n * static_cast<int>(sizeof(T)) + 15 - static_cast<int>(sizeof(T))) / 16 + 1;
+}
 constexpr int kNormNarrow = 256;  // threads of a CTA of narrow rows
 
 struct NormArgs {
@@ -775,6 +780,216 @@ __global__ void __launch_bounds__(NARROW ? kNormNarrow : 1024, NARROW || NV > 2 
       if (live && a.dgate) static_cast<T*>(a.dgate)[row * a.n + c] = from_f32<T>(Ds * t * slope);
       if (live && a.dy) static_cast<T*>(a.dy)[row * a.n + c] = from_f32<T>(fmaf(y[i], -ky, Ds * act * post * r1));
     }
+  }
+  if (a.partial) put_sums<NV, 1, NARROW>(a, sums, cols, lane, sub, per);
+}
+
+// -- many rows on any address of tensors that start on 16 bytes -------------------------
+//
+// CTAs stay.  The aligned 16-byte units that cover a group's next row travel by
+// cp.async into its places in shared memory, [2][tensors][units], while this row is
+// worked on, and are read at the row's own shift; weights stay in registers.  The
+// arithmetic is that of the kernels above: with both forms in one template, those
+// lost 10 to 50% to registers they have not got.
+template <typename T, bool NARROW>
+struct AheadRows {
+  unsigned char* mine;  // this group's places
+  int tensors, units, lane, tpr, n;
+  long long bytes;      // of a tensor
+  int stage = 0;
+
+  __device__ __forceinline__ AheadRows(const NormArgs& a, unsigned char* ring, int tensors, int sub, int lane, int tpr)
+      : tensors(tensors), units(ahead_units<T>(a.n)), lane(lane), tpr(tpr), n(a.n), bytes(a.rows * a.n * static_cast<long long>(sizeof(T))) {
+    mine = ring + static_cast<long long>(sub) * 2 * tensors * units * 16;
+  }
+  __device__ __forceinline__ unsigned char* place(int st, int k) const { return mine + (st * tensors + k) * units * 16; }
+  __device__ __forceinline__ void fetch(int st, int k, const void* p, long long row) const {
+    const long long from = row * n * static_cast<long long>(sizeof(T)), at = from & ~15ll;
+    const int need = static_cast<int>(from - at) + n * static_cast<int>(sizeof(T));
+    for (int u = lane; u * 16 < need; u += tpr) {
+      const long long left = bytes - at - 16 * u;  // of the tensor, at least 1
+      copy_async16(place(st, k) + u * 16, static_cast<const unsigned char*>(p) + at + 16 * u, left < 16 ? static_cast<int>(left) : 16);
+    }
+  }
+  // Everything that fetch() was called for is there, for the whole group.
+  __device__ __forceinline__ void turn() {
+    copy_wait<0>();
+    if constexpr (NARROW) __syncwarp();
+    else __syncthreads();
+  }
+  __device__ __forceinline__ float get(int k, const void* p, long long row, int c, bool live) const {
+    if (!live || !p) return 0.f;
+    const int shift = static_cast<int>(static_cast<unsigned>(row) * static_cast<unsigned>(n) % (16 / sizeof(T)));
+    return to_f32(reinterpret_cast<const T*>(place(stage, k))[shift + c]);
+  }
+};
+
+// A thread's channels of a weight vector.
+template <int NV>
+struct AheadWeight {
+  float w[NV];
+  __device__ __forceinline__ AheadWeight(const float* p, int n, int tpr, int lane) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) w[i] = load_weight(p, i * tpr + lane, i * tpr + lane < n);
+  }
+};
+
+// Narrow: a warp a row.
+template <typename T, int NV, bool NARROW>
+__global__ void __launch_bounds__(NARROW ? kNormNarrow : 512, NARROW ? 3 : 2) norm_ahead_kernel(NormArgs a) {
+  __shared__ float sm[2][32][4];
+  extern __shared__ __align__(16) unsigned char ahead_places[];
+  int turn = 0;
+  const int tpr = NARROW ? 32 : a.tpr;
+  const int lane = NARROW ? static_cast<int>(threadIdx.x) % tpr : static_cast<int>(threadIdx.x);
+  const int per = NARROW ? kNormNarrow / tpr : 1, sub = NARROW ? static_cast<int>(threadIdx.x) / tpr : 0;
+  const float inv = 1.f / static_cast<float>(a.n);
+  const int kg = 1, kr = kg + (a.gate != nullptr);
+  AheadRows<T, NARROW> in(a, ahead_places, kr + (a.residual != nullptr), sub, lane, tpr);
+  const AheadWeight<NV> post(a.post, a.n, tpr, lane), scale(a.scale, a.n, tpr, lane), pre(a.pre, a.n, tpr, lane);
+  auto fetch = [&](int st, long long row) {
+    if (row < a.rows) {
+      in.fetch(st, 0, a.y, row);
+      if (a.gate) in.fetch(st, kg, a.gate, row);
+      if (a.residual) in.fetch(st, kr, a.residual, row);
+    }
+    copy_commit();
+  };
+  const long long step = static_cast<long long>(gridDim.x) * per;
+  fetch(0, static_cast<long long>(blockIdx.x) * per + sub);
+  for (long long first = static_cast<long long>(blockIdx.x) * per; first < a.rows; first += step) {
+    const long long row = first + sub;
+    const bool here = row < a.rows && wanted(a, row);
+    in.turn();
+    fetch(in.stage ^ 1, row + step);
+    float y[NV], g[NV], o[NV], ss[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = i * tpr + lane;
+      const bool live = here && c < a.n;
+      y[i] = in.get(0, a.y, row, c, live);
+      g[i] = in.get(kg, a.gate, row, c, live);
+      o[i] = in.get(kr, a.residual, row, c, live);
+      ss[0] = fmaf(y[i], y[i], ss[0]);
+    }
+    float r1 = 1.f;
+    if (a.post) {
+      row_sum<1, NARROW>(ss, tpr, sm, turn);
+      r1 = rsqrtf(fmaf(ss[0], inv, a.eps));
+    }
+    ss[0] = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = i * tpr + lane;
+      const bool live = here && c < a.n;
+      float u = y[i] * r1 * post.w[i];
+      if (a.gate) u *= g[i] * sigmoid(g[i]);
+      o[i] = fmaf(scale.w[i], u, o[i]);
+      ss[0] = fmaf(o[i], o[i], ss[0]);
+      if (live && a.out) static_cast<T*>(a.out)[row * a.n + c] = from_f32<T>(o[i]);
+    }
+    float r2 = 1.f;
+    if (a.pre) {
+      row_sum<1, NARROW>(ss, tpr, sm, turn);
+      r2 = rsqrtf(fmaf(ss[0], inv, a.eps));
+    }
+    if (a.stats && here && lane == 0) *reinterpret_cast<float2*>(a.stats + 2 * row) = make_float2(r1, r2);
+    in.stage ^= 1;
+    if (!a.pre) continue;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = i * tpr + lane;
+      if (here && c < a.n) static_cast<T*>(a.normed)[row * a.n + c] = from_f32<T>(o[i] * r2 * pre.w[i]);
+    }
+  }
+}
+
+template <typename T, int NV, bool NARROW>
+__global__ void __launch_bounds__(NARROW ? kNormNarrow : 512, NARROW ? 2 : 1) norm_backward_ahead_kernel(NormArgs a) {
+  __shared__ float sm[2][32][4];
+  extern __shared__ __align__(16) unsigned char ahead_places[];
+  float* const cols = reinterpret_cast<float*>(ahead_places);  // after the rows; narrow: [256 / tpr][n] of one parameter at a time
+  int turn = 0;
+  const int tpr = NARROW ? 32 : a.tpr;
+  const int lane = NARROW ? static_cast<int>(threadIdx.x) % tpr : static_cast<int>(threadIdx.x);
+  const int per = NARROW ? kNormNarrow / tpr : 1, sub = NARROW ? static_cast<int>(threadIdx.x) / tpr : 0;
+  const float inv = 1.f / static_cast<float>(a.n);
+  float sums[3][NV][1];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) sums[0][i][0] = sums[1][i][0] = sums[2][i][0] = 0.f;
+
+  const void* const residual = a.pre ? a.residual : nullptr;
+  const int kg = 1, kd = kg + (a.gate != nullptr), kr = kd + (a.dout != nullptr), kp = kr + (residual != nullptr);
+  AheadRows<T, NARROW> in(a, ahead_places, kp + (a.dnormed != nullptr), sub, lane, tpr);
+  const AheadWeight<NV> wpost(a.post, a.n, tpr, lane), wscale(a.scale, a.n, tpr, lane), wpre(a.pre, a.n, tpr, lane);
+  auto fetch = [&](int st, long long row) {
+    if (row < a.rows) {
+      in.fetch(st, 0, a.y, row);
+      if (a.gate) in.fetch(st, kg, a.gate, row);
+      if (a.dout) in.fetch(st, kd, a.dout, row);
+      if (residual) in.fetch(st, kr, residual, row);
+      if (a.dnormed) in.fetch(st, kp, a.dnormed, row);
+    }
+    copy_commit();
+  };
+  const long long step = static_cast<long long>(gridDim.x) * per;
+  fetch(0, static_cast<long long>(blockIdx.x) * per + sub);
+  for (long long first = static_cast<long long>(blockIdx.x) * per; first < a.rows; first += step) {
+    const long long row = first + sub;
+    in.turn();
+    fetch(in.stage ^ 1, row + step);
+    float y[NV], g[NV], D[NV], pn[NV], x[NV], v[4] = {0.f, 0.f, 0.f, 0.f};  // v: S1 to S4
+    const float2 r = a.stats && row < a.rows ? __ldg(reinterpret_cast<const float2*>(a.stats) + row) : make_float2(1.f, 1.f);
+    const float r1 = r.x, r2 = r.y;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = i * tpr + lane;
+      const bool live = row < a.rows && c < a.n;
+      y[i] = in.get(0, a.y, row, c, live);
+      g[i] = in.get(kg, a.gate, row, c, live);
+      D[i] = in.get(kd, a.dout, row, c, live);
+      x[i] = in.get(kr, residual, row, c, live);
+      pn[i] = in.get(kp, a.dnormed, row, c, live);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const float scale = wscale.w[i], d = pn[i] * wpre.w[i];
+      float u = y[i] * r1 * wpost.w[i];
+      if (a.gate) u *= g[i] * sigmoid(g[i]);
+      x[i] = fmaf(scale, u, x[i]);  // out from here on
+      u *= scale;
+      v[0] = fmaf(d, x[i], v[0]);
+      v[1] = fmaf(u, D[i], v[1]);
+      v[2] = fmaf(u, d, v[2]);
+      v[3] = fmaf(u, x[i], v[3]);
+    }
+    if (a.post || a.pre) row_sum<4, NARROW>(v, tpr, sm, turn);
+    const float k = a.pre ? v[0] * inv * r2 : 0.f;  // mean(d on)
+    const float ky = a.post ? (a.pre ? fmaf(r2, fmaf(-k * r2, v[3], v[2]), v[1]) : v[1]) * inv * r1 * r1 : 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = i * tpr + lane;
+      const bool live = row < a.rows && c < a.n;
+      const float post = wpost.w[i], scale = wscale.w[i], yn = y[i] * r1;
+      if (a.pre) {
+        const float on = x[i] * r2;
+        sums[2][i][0] = fmaf(pn[i], on, sums[2][i][0]);
+        D[i] = fmaf(r2, pn[i] * wpre.w[i] - on * k, D[i]);
+      }
+      float act = 1.f, slope = 0.f;
+      if (a.gate) {
+        const float sg = sigmoid(g[i]);
+        act = g[i] * sg;
+        slope = fmaf(act, 1.f - sg, sg);
+      }
+      const float Ds = D[i] * scale, t = post * yn;
+      sums[0][i][0] = fmaf(Ds * act, yn, sums[0][i][0]);
+      sums[1][i][0] = fmaf(D[i] * act, t, sums[1][i][0]);
+      if (live && a.dresidual) static_cast<T*>(a.dresidual)[row * a.n + c] = from_f32<T>(D[i]);
+      if (live && a.dgate) static_cast<T*>(a.dgate)[row * a.n + c] = from_f32<T>(Ds * t * slope);
+      if (live && a.dy) static_cast<T*>(a.dy)[row * a.n + c] = from_f32<T>(fmaf(y[i], -ky, Ds * act * post * r1));
+    }
+    in.stage ^= 1;
   }
   if (a.partial) put_sums<NV, 1, NARROW>(a, sums, cols, lane, sub, per);
 }

@@ -150,6 +150,38 @@ def test_many_rows(rows, D, parts, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("parts", [ALL, ("post_weight", "gate"), ("residual", "pre_weight"), ("scale",)], ids="-".join)
+@pytest.mark.parametrize("rows,D", [(2960, 33), (2961, 65), (5003, 95), (2977, 127), (9000, 163), (2963, 255), (4000, 257), (2999, 511),
+                                    (2960, 513), (3001, 1001), (2965, 2047)])
+def test_many_odd_rows(rows, D, parts, dtype):
+    """Rows on any address, enough of them that the next is fetched ahead."""
+    compare(make(rows, D, 1, dtype, 9, parts), 1, 1e-6, dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_many_odd_heads(dtype):
+    compare(make(500, 7 * 163, 7, dtype, 10, ("post_weight", "gate", "residual")), 7, 1e-6, dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D", [163, 301])
+def test_many_odd_rows_in_place_and_skipped(D, dtype):
+    from recurrent_state_update_deltalog_b200 import DeltaLog, block_norm
+    gen = torch.Generator(device="cuda").manual_seed(D)
+    rows = 3333
+    y, g, r = (torch.randn(rows, D, device="cuda", generator=gen).to(dtype) for _ in range(3))
+    w, w2 = (torch.rand(D, device="cuda", generator=gen) + 0.5 for _ in range(2))
+    out, normed = block_norm(y, w, g, None, r, w2)
+    idx = torch.arange(rows, dtype=torch.int32, device="cuda")
+    idx[5::7] = -1
+    idx[3::11] |= DeltaLog.HOLD
+    skipped = (idx < 0) | (idx & DeltaLog.HOLD != 0)
+    y2, r2 = y.clone(), r.clone()
+    block_norm(y2, w, g, None, r2, w2, slot_idx=idx, slots=rows, out=r2, normed_out=y2)
+    assert torch.equal(r2, torch.where(skipped[:, None], r, out)) and torch.equal(y2, torch.where(skipped[:, None], y, normed))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("rows,H,d", [(1, 1, 64), (5, 3, 64), (700, 4, 128), (3, 7, 33), (2, 5, 300), (1500, 2, 16)])
 @pytest.mark.parametrize("parts", [("post_weight", "gate"), ("post_weight", "residual")], ids="-".join)
 def test_groups(rows, H, d, parts, dtype):
