@@ -441,7 +441,7 @@ int dl_scan_backward(int rows, const int* cu_seqlens, long long total, int C, in
 
 /* One token of dl_scan for every row: x, h typed [rows][C], log_decay float
  * [rows][C], state and new_state float [slots][C] (new_state may be state;
- * slots that no row names are not written). */
+ * slots that no row names are not written; rows must name distinct slots). */
 int dl_scan_step(const int* slot_idx, int slots, int rows, int C, int in_dtype, const void* x,
                  const float* log_decay, const float* state, float* new_state, void* h,
                  int* dev_err, void* stream);
@@ -498,11 +498,13 @@ int dl_block_norm_backward(int rows, int D, int groups, int in_dtype, const void
  *               (DL_DEVERR_PAGE).  Entries past a row's length are not read;
  *   q, out      typed [rows][Hq][d] (out may be q);
  *   k, v        typed [rows][Hkv][d], the new token's, stored at position
- *               lens[s] - 1 and used from here; both NULL: already stored.
+ *               lens[s] - 1 and used from here (slots distinct, and no other
+ *               row's page); both NULL: already stored, slots may repeat.
  * Hq a multiple of Hkv; d in {64, 128}; page_size a power of two; num_pages *
- * Hkv * page_size < 2^31; pointers of typed tensors 16-byte aligned.  The split over the length follows max_pages
- * (or the window), so a table no wider than needed is fastest.  Scores and
- * sums are fp32; with bf16 the weights enter their product with v as bf16.
+ * Hkv * page_size < 2^31; pointers of typed tensors 16-byte aligned.  The
+ * split over the length follows max_pages (or the window), so a table no wider
+ * than needed is fastest.  Scores and sums are fp32; with bf16 the weights
+ * enter their product with v as bf16.
  *   workspace   16-byte aligned buffer of dl_paged_attention_workspace bytes
  *               (0 where tables are short), not to be used by two calls that
  *               may overlap; NULL: a coarser split, slower on long tables. */
@@ -516,7 +518,8 @@ int dl_paged_attention(const int* slot_idx, int slots, int rows, int Hq, int Hkv
 
 /* Copy prompts into the pages: tokens [cu_seqlens[r], cu_seqlens[r + 1]) of k
  * and v (typed [total][Hkv][d]) to positions starts[s] + 0, 1, ... of row r's
- * slot s (starts device int32 [slots], or NULL: 0).  A row whose range is
+ * slot s (starts device int32 [slots], or NULL: 0); positions written must not
+ * be shared by two rows.  A row whose range is
  * invalid or passes max_pages * page_size is skipped (DL_DEVERR_SEQLEN). */
 int dl_paged_write(const int* slot_idx, int slots, int rows, const int* cu_seqlens, long long total,
                    int Hkv, int d, int in_dtype, int page_size, long long num_pages, int max_pages,

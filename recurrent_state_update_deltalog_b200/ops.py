@@ -112,8 +112,8 @@ def gated_scan_prefill(x, log_decay, state, cu_seqlens, slot_idx=None, zero_stat
 def gated_scan_step(x, log_decay, state, slot_idx=None, new_state=None, out=None, err=None, stream=None):
     """One token of :func:`gated_scan` for rows of a pool of states: x, log_decay
     [rows, C]; row r runs on ``state[slot_idx[r]]`` (fp32 [slots, C]), updated in
-    place, or into ``new_state`` if given.  Rows with a negative or held slot are
-    skipped, their outputs not written.  Returns h [rows, C]."""
+    place, or into ``new_state`` if given; rows name distinct slots.  Rows with a
+    negative or held slot are skipped, their outputs not written.  Returns h [rows, C]."""
     return _call(_scan_step, x, stream, log_decay, state, slot_idx, new_state, out, err)
 
 
@@ -164,7 +164,8 @@ def paged_attention(q, k_pages, v_pages, block_table, lens, k=None, v=None, slot
     page_size, d] of the same type; block_table int32 [slots, max_pages]; lens int32
     [slots], the new token included; row r runs on slot ``slot_idx[r]`` (default r;
     negative or held: skipped, its output not written).  With k, v [rows, Hkv, d] the
-    new token is stored at position lens - 1 first.  ``window`` > 0 keeps the last
+    new token is stored at position lens - 1 first; rows then name distinct slots whose
+    last pages no other row reads.  ``window`` > 0 keeps the last
     ``window`` positions.  scale defaults to d ** -0.5.  A slot of length 0 gives zeros."""
     return _call(_attention, q, stream, k_pages, v_pages, block_table, lens, k, v, slot_idx, window, scale, out, err)
 
